@@ -26,9 +26,10 @@
  *
  * Conventions for every entry point:
  *  - Layouts are row-major and contiguous: q, k, v, out are [B, H, N, d_h];
- *    dt_p is [B, H, N]; A_log and dt_bias are [H]; D is [H*d_h].
+ *    dt_p is [B, H, N]; A_log and dt_bias are [H]; D is [H*d_h].  The gated
+ *    linear recurrence and the norms take strided views (ssd_view, ssd_rows).
  *  - Pointers marked "device" must point to device memory of the current
- *    CUDA device, 16-byte aligned.  The caller owns every buffer; the library
+ *    CUDA device, 16-byte aligned (where not stated otherwise).  The caller owns every buffer; the library
  *    allocates no memory and keeps no state between calls, so calls on
  *    different streams with different buffers are independent.
  *  - Work is enqueued asynchronously on `stream` (a cudaStream_t passed as
@@ -372,6 +373,192 @@ int ssd_fwd_conv(const void *xq, const void *xk, const void *xv, const ssd_conv_
                  const float *log_decay, int B, int H, int N, int d_h, int dtype, int order,
                  int normalize, int chunk, int flags, void *out, void *workspace,
                  size_t workspace_bytes, void *stream);
+
+/*
+ * A strided activation [B, H, N, d_h]: element (b, h, t, c) is at
+ * ptr + b stride_b + h stride_h + t stride_n + c, strides in elements.  Both
+ * the operator's layout (stride_n = d_h) and a slice of a token-major
+ * projection [B, N, ..., H, d_h] are views.  Strides are >= 0; an input may
+ * have stride 0 (broadcast), the elements of an output must be distinct
+ * (nested strides), SSD_ERR_SHAPE otherwise.  The struct itself is in host
+ * memory and is read during the call.
+ */
+typedef struct {
+    void *ptr;
+    long long stride_b, stride_h, stride_n;
+} ssd_view;
+
+/* Option bits of the gated linear recurrence (with SSD_VALUE_DT = 1). */
+typedef enum {
+    SSD_GLR_LOG_DECAY = 2, /* gate holds log a itself; A_log and dt_bias are not read */
+    SSD_GLR_COMPLEMENT = 4 /* value factor f = 1 - a (convex gating) */
+} ssd_glr_flags;
+
+/* Tokens per saved state of ssd_glr_fwd(). */
+#define SSD_GLR_CHUNK 16
+
+/*
+ * Gated linear recurrence: the vector-state form of Algorithm 6 (2Mamba2Furious), with
+ * a decay per channel and token instead of one per head.  For channel
+ * c = h*d_h + j of batch b:
+ *     dt_t    = softplus(gate_t + dt_bias[c])
+ *     log a_t = -exp(A_log[c]) dt_t        or gate_t with SSD_GLR_LOG_DECAY
+ *     f_t     = 1, dt_t (SSD_VALUE_DT) or 1 - a_t (SSD_GLR_COMPLEMENT)
+ *     h_t     = a_t h_{t-1} + f_t x_t,     out_t = h_t
+ * A gate of -infinity leaves the state as it is (a = 1; f = 0 except for
+ * f = 1), a log-decay of -infinity restarts it (a = 0) where h_{t-1} is finite.
+ *   x, gate    device views, element type `dtype`
+ *   A_log      device, [H*d_h] fp32, or NULL (decay rate 1)
+ *   dt_bias    device, [H*d_h] fp32, or NULL (0)
+ *   h0         device, [B, H, d_h] fp32, the state before token 0, or NULL (0)
+ *   lengths    device, [B] int32, or NULL: only tokens t < lengths[b] count
+ *              (values are clamped to [0, N]).  The others are not used, out
+ *              is 0 there, and h_out is the state after token lengths[b] - 1
+ *   out        device view, `dtype`; must not overlap an input
+ *   h_out      device, [B, H, d_h] fp32, or NULL; may equal h0
+ *   states     device, [B, H, ceil(N / SSD_GLR_CHUNK), d_h] fp32, or NULL:
+ *              the state before every SSD_GLR_CHUNK-th token, which
+ *              ssd_glr_bwd() reads
+ * B, H, N, d_h >= 1, any d_h.  Views of any alignment of their element type
+ * are taken; fp32 arrays are 4-byte aligned.  Gates, states and
+ * products are fp32; out is rounded once.  Results do not depend on the
+ * stream, on other calls or on the layout of the views.
+ * Errors: SSD_ERR_NULL, SSD_ERR_DTYPE, SSD_ERR_SHAPE, SSD_ERR_FLAGS (unknown
+ * bits; SSD_VALUE_DT with either of the others), SSD_ERR_ALIGN, SSD_ERR_CUDA.
+ */
+int ssd_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias,
+                const float *h0, const int *lengths, int B, int H, int N, int d_h, int dtype, int flags,
+                const ssd_view *out, float *h_out, float *states, void *stream);
+
+/* Bytes of device workspace ssd_glr_bwd() needs; 0 for invalid arguments. */
+size_t ssd_glr_bwd_workspace_bytes(int B, int H, int N, int d_h, int dtype, int flags);
+
+/*
+ * Gradients of ssd_glr_fwd().  With l_t = dy_t + a_{t+1} l_{t+1} (l of the
+ * last token that counts also receives dh_out):
+ *     dx_t = f_t l_t;  d(log a_t) = a_t l_t h_{t-1} [- a_t l_t x_t with
+ *     SSD_GLR_COMPLEMENT];  the chain through log a, f and softplus gives
+ *     dgate_t;  dA_log[c] and ddt_bias[c] sum over b and t;  dh0 = a_0 l_0.
+ *   dy         device view, `dtype`: gradient of out
+ *   x, gate, A_log, dt_bias, lengths, flags   as given to ssd_glr_fwd()
+ *   states     device, as ssd_glr_fwd() wrote them (they stand for h0)
+ *   dh_out     device, [B, H, d_h] fp32: gradient of h_out, or NULL (0)
+ *   dx, dgate  device views, `dtype`; 0 at tokens that do not count; must not
+ *              overlap an input or each other
+ *   dA_log, ddt_bias  device, [H*d_h] fp32, or NULL; NULL with
+ *              SSD_GLR_LOG_DECAY (SSD_ERR_FLAGS otherwise)
+ *   dh0        device, [B, H, d_h] fp32, or NULL; may equal dh_out
+ *   workspace  device, >= ssd_glr_bwd_workspace_bytes(), 256-byte aligned
+ * h is recomputed in fp32 from `states`; sums over tokens are fp32 in a fixed
+ * order.  Errors as ssd_glr_fwd(), plus SSD_ERR_WORKSPACE.
+ */
+int ssd_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, const float *A_log,
+                const float *dt_bias, const float *states, const int *lengths, const float *dh_out,
+                int B, int H, int N, int d_h, int dtype, int flags, const ssd_view *dx,
+                const ssd_view *dgate, float *dA_log, float *ddt_bias, float *dh0, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+/*
+ * One token of ssd_glr_fwd() per sequence, for generation after a prefill:
+ * x, gate, out are views of [B, H, 1, d_h] (stride_n is not used), h
+ * ([B, H, d_h] fp32, device) is updated in place.  One launch.
+ */
+int ssd_glr_step(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias, int B,
+                 int H, int d_h, int dtype, int flags, float *h, const ssd_view *out, void *stream);
+
+/* Option bits of ssd_norm_params. */
+typedef enum { SSD_NORM_GATE_AFTER = 1 } ssd_norm_flags;
+
+/* Parameters of the norms, in host memory. */
+typedef struct {
+    float eps;  /* > 0, added to the mean square */
+    int groups; /* gated norm: the H*d_h channels are normalised in this many equal groups */
+    int flags;  /* gated norm: 0 or SSD_NORM_GATE_AFTER */
+} ssd_norm_params;
+
+/* A matrix of rows: element (m, c) is at ptr + m stride + c (stride in elements, >= 0;
+ * of an output >= C).  The struct is in host memory. */
+typedef struct {
+    void *ptr;
+    long long stride;
+} ssd_rows;
+
+/*
+ * Residual add and root-mean-square norm before a block:
+ *     r = residual + scale (.) x            rounded to `res_dtype`
+ *     out = r / sqrt(mean_c(r^2) + eps) (.) w
+ *   x          device rows [M, C], element type `dtype` (a block's output)
+ *   residual   device rows [M, C], element type `res_dtype`, or NULL (0)
+ *   scale      device, [C] fp32, or NULL (1)
+ *   w          device, [C] fp32, or NULL (1)
+ *   r          device rows, `res_dtype`: the new residual stream; may be
+ *              `residual` itself (updated in place); NULL when residual
+ *              and scale are NULL and the types are equal: then r = x
+ *   out        device rows [M, C], `dtype`
+ *   rstd       device, [M] fp32: 1 / sqrt(mean + eps), or NULL
+ *   p          eps (groups and flags are not used)
+ * res_dtype is `dtype` or SSD_F32.  The norm is of r as stored, so a later
+ * reader of the stream sees what was normalised.  Sums are fp32.
+ * M, C >= 1.  Errors: SSD_ERR_NULL, SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes,
+ * strides, eps), SSD_ERR_ALIGN (element alignment), SSD_ERR_CUDA.
+ */
+int ssd_add_norm(const ssd_rows *x, const ssd_rows *residual, const float *scale, const float *w, int M,
+                 int C, int dtype, int res_dtype, const ssd_norm_params *p, const ssd_rows *r,
+                 const ssd_rows *out, float *rstd, void *stream);
+
+/* Bytes of device workspace ssd_add_norm_bwd() needs; 0 for invalid sizes. */
+size_t ssd_add_norm_bwd_workspace_bytes(int M, int C);
+
+/*
+ * Gradients of ssd_add_norm(), with xhat = r rstd and g = dy (.) w:
+ *     dr = rstd (g - xhat mean_c(g xhat)) + dres,   dx = scale (.) dr,
+ *     dw = sum_m dy (.) xhat,                       dscale = sum_m dr (.) x.
+ *   dy     device rows, `dtype`: gradient of out
+ *   r      device rows, `res_dtype`: the stream that was normalised
+ *   rstd   device, [M] fp32, as ssd_add_norm() wrote it
+ *   x      device rows, `dtype`; read for dscale only (else may be NULL)
+ *   dres   device rows, `res_dtype`: gradient of r from its other readers, or NULL (0)
+ *   dr     device rows, `res_dtype`: gradient of `residual`; may be dres itself
+ *   dx     device rows, `dtype`, or NULL when not wanted (without a scale and
+ *          with equal types it equals dr)
+ *   dw, dscale  device, [C] fp32, or NULL
+ *   workspace   device, >= ssd_add_norm_bwd_workspace_bytes(), 256-byte aligned
+ */
+int ssd_add_norm_bwd(const ssd_rows *dy, const ssd_rows *r, const float *rstd, const float *w,
+                     const ssd_rows *x, const float *scale, const ssd_rows *dres, int M, int C, int dtype,
+                     int res_dtype, const ssd_rows *dr, const ssd_rows *dx, float *dw, float *dscale,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated root-mean-square norm behind the operator, over the H*d_h channels of a
+ * token in p->groups equal groups (vec(y) of Algorithm 1 with the gate
+ * Z = h W_z of Algorithm 3):
+ *     u = x SiLU(z),  out = u / sqrt(mean_group(u^2) + eps) (.) w
+ *     with SSD_NORM_GATE_AFTER:  out = x / sqrt(mean_group(x^2) + eps) (.) w SiLU(z)
+ *   x      device view, `dtype` (the operator's output [B, H, N, d_h])
+ *   z      device view, `dtype`, or NULL (no gate)
+ *   w      device, [H*d_h] fp32, or NULL (1)
+ *   out    device view, `dtype`: stride_h = d_h, stride_n = H*d_h writes the
+ *          rows that an output projection reads
+ *   rstd   device, [B, N, groups] fp32, or NULL
+ * groups divides H*d_h (SSD_ERR_SHAPE otherwise).  Errors as ssd_add_norm(),
+ * plus SSD_ERR_FLAGS.
+ */
+int ssd_gated_norm(const ssd_view *x, const ssd_view *z, const float *w, int B, int H, int N, int d_h,
+                   int dtype, const ssd_norm_params *p, const ssd_view *out, float *rstd, void *stream);
+
+/* Bytes of device workspace ssd_gated_norm_bwd() needs; 0 for invalid sizes. */
+size_t ssd_gated_norm_bwd_workspace_bytes(int B, int H, int N, int d_h, int groups);
+
+/*
+ * Gradients of ssd_gated_norm().  dy, dx, dz are views like out, x, z (dz NULL
+ * exactly when z is NULL); rstd as ssd_gated_norm() wrote it; dw [H*d_h] fp32
+ * or NULL; workspace as for ssd_add_norm_bwd().
+ */
+int ssd_gated_norm_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *z, const float *w,
+                       const float *rstd, int B, int H, int N, int d_h, int dtype,
+                       const ssd_norm_params *p, const ssd_view *dx, const ssd_view *dz, float *dw,
+                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Test hook for the device-side failure detection; the pages have no

@@ -1,16 +1,19 @@
 """B200 (sm_100a) implementation of the decay-masked linear-attention (SSD)
-forward operator of Mamba-2 / Mamba-2S / 2Mamba.
+forward operator of Mamba-2 / Mamba-2S / 2Mamba, the gated linear recurrence,
+and the norms around a block.
 
 This module is a thin ctypes binding over libssd.so (C ABI in
 include/ssd.h).  It only marshals arguments: every step of the operator runs
-in the library's CUDA kernels.  Tensors are torch tensors; device tensors must
-be contiguous and live on the current CUDA device.  If libssd.so has not been
+in the library's CUDA kernels.  Tensors are torch tensors; device tensors
+live on the current CUDA device and are contiguous, except where a function
+takes strided ones.  If libssd.so has not been
 built, every call raises -- there is no fallback implementation.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,10 @@ SSD_BF16 = 1
 SSD_VALUE_DT = 1  # ssd_fwd_ex flag: contract with v * dt (Algorithm 4, V_dt)
 SSD_STATE_H = 1   # state-mask bits for ssd_workspace_bytes_ex
 SSD_STATE_Z = 2
+SSD_GLR_LOG_DECAY = 2   # ssd_glr_fwd flags: the gate is log a itself
+SSD_GLR_COMPLEMENT = 4  # value factor 1 - a
+SSD_GLR_CHUNK = 16      # tokens per saved state of ssd_glr_fwd
+SSD_NORM_GATE_AFTER = 1
 PATH_NAMES = {0: "simt", 1: "tc_order1", 2: "tc_order2", 3: "tc_order2_quad"}
 
 _lib = None
@@ -84,6 +91,26 @@ def load_library():
     lib.ssd_fwd_path.restype = ci
     lib.ssd_debug_fwd.argtypes = [vp] * 7 + [ci] * 8 + [vp, vp, sz, vp, ci, ctypes.c_longlong, ci]
     lib.ssd_debug_fwd.restype = ci
+    lib.ssd_glr_fwd.argtypes = [vp] * 6 + [ci] * 6 + [vp] * 4
+    lib.ssd_glr_fwd.restype = ci
+    lib.ssd_glr_bwd_workspace_bytes.argtypes = [ci] * 6
+    lib.ssd_glr_bwd_workspace_bytes.restype = sz
+    lib.ssd_glr_bwd.argtypes = [vp] * 8 + [ci] * 6 + [vp] * 6 + [sz, vp]
+    lib.ssd_glr_bwd.restype = ci
+    lib.ssd_glr_step.argtypes = [vp] * 4 + [ci] * 5 + [vp] * 3
+    lib.ssd_glr_step.restype = ci
+    lib.ssd_add_norm.argtypes = [vp] * 4 + [ci] * 4 + [vp] * 5
+    lib.ssd_add_norm.restype = ci
+    lib.ssd_add_norm_bwd_workspace_bytes.argtypes = [ci] * 2
+    lib.ssd_add_norm_bwd_workspace_bytes.restype = sz
+    lib.ssd_add_norm_bwd.argtypes = [vp] * 7 + [ci] * 4 + [vp] * 5 + [sz, vp]
+    lib.ssd_add_norm_bwd.restype = ci
+    lib.ssd_gated_norm.argtypes = [vp] * 3 + [ci] * 5 + [vp] * 4
+    lib.ssd_gated_norm.restype = ci
+    lib.ssd_gated_norm_bwd_workspace_bytes.argtypes = [ci] * 5
+    lib.ssd_gated_norm_bwd_workspace_bytes.restype = sz
+    lib.ssd_gated_norm_bwd.argtypes = [vp] * 5 + [ci] * 5 + [vp] * 5 + [sz, vp]
+    lib.ssd_gated_norm_bwd.restype = ci
     _lib = lib
     return lib
 
@@ -361,3 +388,364 @@ def ssd_conv1d(x, w, bias=None, silu: bool = True, out=None, stream=None):
                                    int(bool(silu)), _dtype_code(x), _ptr(out), _stream_handle(stream))
     _check(rc, "ssd_conv1d")
     return out
+
+
+# ------------------------------------- gated linear recurrence and the norms
+#
+# These take strided tensors (last dimension contiguous).  Each call is
+# enqueued on `stream` (default: the current torch stream); what it allocates
+# belongs to that stream, and tensors given to a call on another stream than
+# the current one are recorded there, so that their memory is not reused early.
+
+_VIEW = struct.Struct("Pqqq")          # include/ssd.h ssd_view
+_ROWS = struct.Struct("Pq")            # include/ssd.h ssd_rows
+_NORM_PARAMS = struct.Struct("fii")    # include/ssd.h ssd_norm_params
+
+
+class _Call:
+    """The tensors and the stream of one call: checks, outputs, the handle."""
+
+    def __init__(self, first, stream):
+        import torch
+        self.torch, self.stream = torch, None
+        self.device = first.device
+        if self.device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            raise ValueError(f"tensors are on {self.device}, which is not the current CUDA device")
+        self.index, self.used = index, []
+        current = torch._C._cuda_getCurrentRawStream(index)
+        if stream is None:
+            self.handle = current
+        else:
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+            self.handle = stream.cuda_stream
+            if self.handle != current:
+                self.stream = stream
+
+    def use(self, t, name, shape, dtype):
+        """Checks a tensor and returns its data pointer; None passes through."""
+        if t is None:
+            return None
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} must be on {self.device}")
+        if self.stream is not None:
+            self.used.append(t)
+        return t.data_ptr()
+
+    def flat(self, t, name, shape, dtype=None):
+        """A contiguous float32 (or `dtype`) array's pointer."""
+        if t is None:
+            return None
+        p = self.use(t, name, shape, dtype or self.torch.float32)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return p
+
+    def new(self, shape, dtype):
+        """An output or workspace tensor that belongs to the call's stream."""
+        if self.stream is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.stream):
+            t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        return t
+
+    def done(self, rc, where):
+        for t in self.used:
+            t.record_stream(self.stream)
+        if rc != 0:
+            raise SSDError(rc, where)
+
+
+def _inner_contiguous(t, name):
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return st
+
+
+def _heads_view(call, t, name, shape, dtype):
+    """ssd_view of a [B, H, N, d_h] tensor."""
+    if t is None:
+        return None
+    p = call.use(t, name, shape, dtype)
+    st = _inner_contiguous(t, name)
+    return _VIEW.pack(p, st[0], st[1], st[2])
+
+
+def _tokens_view(call, t, name, shape, dtype, d):
+    """ssd_view of a [B, N, H*d_h] tensor."""
+    if t is None:
+        return None
+    p = call.use(t, name, shape, dtype)
+    st = _inner_contiguous(t, name)
+    return _VIEW.pack(p, st[0], d, st[1])
+
+
+def _rows_view(call, t, name, shape, dtype):
+    """ssd_rows of a [..., C] tensor whose leading dimensions have one stride."""
+    if t is None:
+        return None
+    p = call.use(t, name, shape, dtype)
+    st = _inner_contiguous(t, name)
+    step, n = None, 1
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(st[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * n:
+            raise ValueError(f"{name}: the leading dimensions must be evenly spaced (one stride between rows)")
+        n *= size
+    return _ROWS.pack(p, t.shape[-1] if step is None else step)
+
+
+def _glr_gate(dt_p, log_decay, value_dt, value_complement):
+    if (dt_p is None) == (log_decay is None):
+        raise ValueError("give either dt_p or log_decay")
+    if value_dt and (value_complement or dt_p is None):
+        raise ValueError("value_dt needs dt_p, and excludes value_complement")
+    flags = (SSD_VALUE_DT if value_dt else 0) | (SSD_GLR_COMPLEMENT if value_complement else 0)
+    return (dt_p, flags) if log_decay is None else (log_decay, flags | SSD_GLR_LOG_DECAY)
+
+
+def glr_states_shape(B: int, H: int, N: int, d_h: int):
+    """Shape of the saved states of ssd_glr_fwd (one per SSD_GLR_CHUNK tokens)."""
+    return (B, H, -(-N // SSD_GLR_CHUNK), d_h)
+
+
+def alloc_glr_states(B: int, H: int, N: int, d_h: int, device=None):
+    """A float32 buffer for ssd_glr_fwd's `states`."""
+    import torch
+    return torch.empty(glr_states_shape(B, H, N, d_h), dtype=torch.float32, device=device or "cuda")
+
+
+def ssd_glr_fwd(x, dt_p, A_log, dt_bias, log_decay=None, value_dt: bool = False, value_complement: bool = False,
+                h0=None, h_out=None, states=None, lengths=None, out=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + f_t x_t per channel
+    (include/ssd.h, ssd_glr_fwd); returns `out` = h.
+
+    x and the gate (dt_p, or log_decay = log a) are [B, H, N, d_h] float32 or
+    bfloat16 of any strides; A_log, dt_bias [H*d_h] float32 or None.  f is 1,
+    dt (value_dt) or 1 - a (value_complement).  h0, h_out: [B, H, d_h] float32
+    or None; states: alloc_glr_states() to be filled for ssd_glr_bwd; lengths:
+    [B] int32, the tokens of each sequence that count."""
+    gate, flags = _glr_gate(dt_p, log_decay, value_dt, value_complement)
+    B, H, N, d = shape = x.shape
+    call = _Call(x, stream)
+    dt = _dtype_code(x)
+    if out is None:
+        out = call.new(shape, x.dtype)
+    C = (H * d,)
+    rc = load_library().ssd_glr_fwd(
+        _heads_view(call, x, "x", shape, x.dtype), _heads_view(call, gate, "the gate", shape, x.dtype),
+        call.flat(A_log, "A_log", C), call.flat(dt_bias, "dt_bias", C), call.flat(h0, "h0", (B, H, d)),
+        call.flat(lengths, "lengths", (B,), call.torch.int32), B, H, N, d, dt, flags,
+        _heads_view(call, out, "out", shape, x.dtype), call.flat(h_out, "h_out", (B, H, d)),
+        call.flat(states, "states", glr_states_shape(B, H, N, d)), call.handle)
+    call.done(rc, "ssd_glr_fwd")
+    return out
+
+
+def ssd_glr_bwd_workspace_bytes(B: int, H: int, N: int, d_h: int, dtype: int, flags: int = 0) -> int:
+    """Device workspace (bytes) ssd_glr_bwd needs; 0 when invalid."""
+    return int(load_library().ssd_glr_bwd_workspace_bytes(B, H, N, d_h, dtype, flags))
+
+
+def ssd_glr_bwd(dy, x, dt_p, A_log, dt_bias, states, log_decay=None, value_dt: bool = False,
+                value_complement: bool = False, lengths=None, dh_out=None, dx=None, dgate=None, workspace=None,
+                stream=None):
+    """Gradients of ssd_glr_fwd (include/ssd.h, ssd_glr_bwd), from its `states`.
+
+    dy: [B, H, N, d_h], gradient of out; dh_out: [B, H, d_h] float32, gradient
+    of h_out, or None.  Returns (dx, dgate, dA_log, ddt_bias, dh0): dgate is
+    the gradient of dt_p or log_decay; dA_log and ddt_bias are None where the
+    parameter is."""
+    gate, flags = _glr_gate(dt_p, log_decay, value_dt, value_complement)
+    B, H, N, d = shape = x.shape
+    call = _Call(x, stream)
+    dt, f32 = _dtype_code(x), call.torch.float32
+    if states is None:
+        raise ValueError("ssd_glr_bwd needs the states that ssd_glr_fwd saved")
+    log = bool(flags & SSD_GLR_LOG_DECAY)
+    C = (H * d,)
+    dA = None if log or A_log is None else call.new(C, f32)
+    db = None if log or dt_bias is None else call.new(C, f32)
+    dh0 = call.new((B, H, d), f32)
+    if dx is None:
+        dx = call.new(shape, x.dtype)
+    if dgate is None:
+        dgate = call.new(shape, x.dtype)
+    if workspace is None:
+        workspace = call.new((max(1, ssd_glr_bwd_workspace_bytes(B, H, N, d, dt, flags)),), call.torch.uint8)
+    rc = load_library().ssd_glr_bwd(
+        _heads_view(call, dy, "dy", shape, x.dtype), _heads_view(call, x, "x", shape, x.dtype),
+        _heads_view(call, gate, "the gate", shape, x.dtype), call.flat(A_log, "A_log", C),
+        call.flat(dt_bias, "dt_bias", C), call.flat(states, "states", glr_states_shape(B, H, N, d)),
+        call.flat(lengths, "lengths", (B,), call.torch.int32), call.flat(dh_out, "dh_out", (B, H, d)),
+        B, H, N, d, dt, flags, _heads_view(call, dx, "dx", shape, x.dtype),
+        _heads_view(call, dgate, "dgate", shape, x.dtype), _ptr(dA), _ptr(db), dh0.data_ptr(),
+        call.flat(workspace, "workspace", workspace.shape, call.torch.uint8), workspace.numel(), call.handle)
+    call.done(rc, "ssd_glr_bwd")
+    return dx, dgate, dA, db, dh0
+
+
+def ssd_glr_step(x, dt_p, A_log, dt_bias, h, log_decay=None, value_dt: bool = False, value_complement: bool = False,
+                 out=None, stream=None):
+    """One token of ssd_glr_fwd per sequence (include/ssd.h, ssd_glr_step): x
+    and the gate [B, H, d_h]; h [B, H, d_h] float32, updated in place.
+    Returns `out` [B, H, d_h]."""
+    gate, flags = _glr_gate(dt_p, log_decay, value_dt, value_complement)
+    B, H, d = shape = x.shape
+    call = _Call(x, stream)
+    dt = _dtype_code(x)
+    if h is None:
+        raise ValueError("ssd_glr_step needs the state h")
+    if out is None:
+        out = call.new(shape, x.dtype)
+
+    def view(t, name):
+        p = call.use(t, name, shape, x.dtype)
+        st = _inner_contiguous(t, name)
+        return _VIEW.pack(p, st[0], st[1], 0)
+
+    rc = load_library().ssd_glr_step(
+        view(x, "x"), view(gate, "the gate"), call.flat(A_log, "A_log", (H * d,)),
+        call.flat(dt_bias, "dt_bias", (H * d,)), B, H, d, dt, flags, call.flat(h, "h", shape), view(out, "out"),
+        call.handle)
+    call.done(rc, "ssd_glr_step")
+    return out
+
+
+def ssd_add_norm(x, residual=None, scale=None, w=None, eps: float = 1e-5, r=None, out=None, rstd=None, stream=None):
+    """Residual add with its scale, then a root-mean-square norm
+    (include/ssd.h, ssd_add_norm): r = residual + scale * x, out = rms_norm(r) * w.
+
+    x: [..., C] float32 or bfloat16; residual: the same shape, x's type or
+    float32, or None; scale, w: [C] float32 or None.  Returns (out, r, rstd):
+    r has the residual's type (it may be given as r=residual, updated in
+    place) and is x itself when there is neither residual nor scale; rstd is
+    [...] float32, for ssd_add_norm_bwd."""
+    shape, C = x.shape, x.shape[-1]
+    M = x.numel() // C if C else 0
+    call = _Call(x, stream)
+    dt, f32 = _dtype_code(x), call.torch.float32
+    res_dtype = x.dtype if residual is None else residual.dtype
+    rt = _dtype_code(x if residual is None else residual)
+    if out is None:
+        out = call.new(shape, x.dtype)
+    if rstd is None:
+        rstd = call.new(shape[:-1], f32)
+    plain = residual is None and scale is None
+    if plain and r is not None:
+        raise ValueError("without residual and scale r is x: none is written")
+    if r is None and not plain:
+        r = call.new(shape, res_dtype)
+    rc = load_library().ssd_add_norm(
+        _rows_view(call, x, "x", shape, x.dtype), _rows_view(call, residual, "residual", shape, res_dtype),
+        call.flat(scale, "scale", (C,)), call.flat(w, "w", (C,)), M, C, dt, rt, _NORM_PARAMS.pack(eps, 1, 0),
+        _rows_view(call, r, "r", shape, res_dtype), _rows_view(call, out, "out", shape, x.dtype),
+        call.flat(rstd, "rstd", shape[:-1]), call.handle)
+    call.done(rc, "ssd_add_norm")
+    return out, x if plain else r, rstd
+
+
+def ssd_add_norm_bwd(dy, r, rstd, w=None, x=None, scale=None, dres=None, dr=None, dx=None, workspace=None,
+                     stream=None):
+    """Gradients of ssd_add_norm (include/ssd.h, ssd_add_norm_bwd).
+
+    dy: [..., C], gradient of out; r, rstd as ssd_add_norm returned them;
+    dres: gradient of r from its other readers, or None.  x is needed when
+    scale is given.  Returns (dr, dx, dw, dscale): dr is the gradient of the
+    residual, dx of x (dr itself without a scale, when the types are equal);
+    dw and dscale are None where the parameter is."""
+    shape, C = dy.shape, dy.shape[-1]
+    M = dy.numel() // C if C else 0
+    call = _Call(dy, stream)
+    dt, f32 = _dtype_code(dy), call.torch.float32
+    rt = _dtype_code(r)
+    if scale is not None and x is None:
+        raise ValueError("the gradient of scale needs x")
+    if dr is None:
+        dr = call.new(shape, r.dtype)
+    same = scale is None and r.dtype == dy.dtype
+    if dx is None and not same:
+        dx = call.new(shape, dy.dtype)
+    dw = None if w is None else call.new((C,), f32)
+    ds = None if scale is None else call.new((C,), f32)
+    if workspace is None:
+        nbytes = int(load_library().ssd_add_norm_bwd_workspace_bytes(M, C))
+        workspace = call.new((max(1, nbytes),), call.torch.uint8)
+    rc = load_library().ssd_add_norm_bwd(
+        _rows_view(call, dy, "dy", shape, dy.dtype), _rows_view(call, r, "r", shape, r.dtype),
+        call.flat(rstd, "rstd", shape[:-1]), call.flat(w, "w", (C,)),
+        None if scale is None else _rows_view(call, x, "x", shape, dy.dtype), call.flat(scale, "scale", (C,)),
+        _rows_view(call, dres, "dres", shape, r.dtype), M, C, dt, rt, _rows_view(call, dr, "dr", shape, r.dtype),
+        _rows_view(call, dx, "dx", shape, dy.dtype), _ptr(dw), _ptr(ds),
+        call.flat(workspace, "workspace", workspace.shape, call.torch.uint8), workspace.numel(), call.handle)
+    call.done(rc, "ssd_add_norm_bwd")
+    return dr, dr if dx is None else dx, dw, ds
+
+
+def ssd_gated_norm(x, z=None, w=None, groups: int = 1, eps: float = 1e-5, gate_after: bool = False, out=None,
+                   rstd=None, stream=None):
+    """Gated root-mean-square norm behind the operator (include/ssd.h,
+    ssd_gated_norm), from head layout to token layout.
+
+    x: [B, H, N, d_h] float32 or bfloat16 of any strides; z: [B, N, H*d_h] gate
+    projection, or None; w: [H*d_h] float32 or None.  The H*d_h channels of a
+    token are normalised in `groups` equal groups, of x SiLU(z), or of x with
+    the gate applied afterwards (gate_after).  Returns (out [B, N, H*d_h], rstd
+    [B, N, groups] float32, for ssd_gated_norm_bwd)."""
+    B, H, N, d = x.shape
+    call = _Call(x, stream)
+    dt, f32 = _dtype_code(x), call.torch.float32
+    tokens = (B, N, H * d)
+    if out is None:
+        out = call.new(tokens, x.dtype)
+    if rstd is None:
+        rstd = call.new((B, N, groups), f32)
+    rc = load_library().ssd_gated_norm(
+        _heads_view(call, x, "x", x.shape, x.dtype), _tokens_view(call, z, "z", tokens, x.dtype, d),
+        call.flat(w, "w", (H * d,)), B, H, N, d, dt,
+        _NORM_PARAMS.pack(eps, groups, SSD_NORM_GATE_AFTER if gate_after else 0),
+        _tokens_view(call, out, "out", tokens, x.dtype, d), call.flat(rstd, "rstd", (B, N, groups)), call.handle)
+    call.done(rc, "ssd_gated_norm")
+    return out, rstd
+
+
+def ssd_gated_norm_bwd(dy, x, rstd, z=None, w=None, groups: int = 1, gate_after: bool = False, dx=None, dz=None,
+                       workspace=None, stream=None):
+    """Gradients of ssd_gated_norm (include/ssd.h, ssd_gated_norm_bwd): dy
+    [B, N, H*d_h]; the others as there.  Returns (dx [B, H, N, d_h],
+    dz [B, N, H*d_h] or None, dw [H*d_h] float32 or None)."""
+    B, H, N, d = x.shape
+    call = _Call(x, stream)
+    dt, f32 = _dtype_code(x), call.torch.float32
+    tokens = (B, N, H * d)
+    if dx is None:
+        dx = call.new(x.shape, x.dtype)
+    if z is None:
+        if dz is not None:
+            raise ValueError("without z there is no dz")
+    elif dz is None:
+        dz = call.new(tokens, x.dtype)
+    dw = None if w is None else call.new((H * d,), f32)
+    if workspace is None:
+        nbytes = int(load_library().ssd_gated_norm_bwd_workspace_bytes(B, H, N, d, groups))
+        workspace = call.new((max(1, nbytes),), call.torch.uint8)
+    rc = load_library().ssd_gated_norm_bwd(
+        _tokens_view(call, dy, "dy", tokens, x.dtype, d), _heads_view(call, x, "x", x.shape, x.dtype),
+        _tokens_view(call, z, "z", tokens, x.dtype, d), call.flat(w, "w", (H * d,)),
+        call.flat(rstd, "rstd", (B, N, groups)), B, H, N, d, dt,
+        _NORM_PARAMS.pack(1.0, groups, SSD_NORM_GATE_AFTER if gate_after else 0),
+        _heads_view(call, dx, "dx", x.shape, x.dtype), _tokens_view(call, dz, "dz", tokens, x.dtype, d), _ptr(dw),
+        call.flat(workspace, "workspace", workspace.shape, call.torch.uint8), workspace.numel(), call.handle)
+    call.done(rc, "ssd_gated_norm_bwd")
+    return dx, dz, dw

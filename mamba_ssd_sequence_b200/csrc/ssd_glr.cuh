@@ -1,0 +1,308 @@
+// Device parts shared by the kernels of the gated linear recurrence
+// (ssd_glr_fwd.cu, ssd_glr_bwd.cu, ssd_glr.cu).
+//
+// A tile is kTok tokens of kCb channels.  A thread holds two neighbouring
+// channels of a segment of SSD_GLR_CHUNK consecutive tokens, so a warp reads
+// whole rows of the tile; the segments of a block follow one another in time,
+// and so do the blocks of a cluster.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+#include "ssd_math.cuh"
+#include "ssd_view.h"
+
+namespace ssd {
+namespace glr {
+
+constexpr int kSeg = SSD_GLR_CHUNK;  // tokens per thread and per saved state
+
+struct Args {
+    ssd_view x, gate, out, dy, dx, dgate;
+    const float *A_log, *dt_bias, *h0, *dh_out;
+    const int *lengths;
+    float *h_out, *states, *dh0, *part;
+    int B, H, N, d, nblk, aligned;
+};
+
+// Gate kinds and value factors, as template arguments.
+enum Mode { kDtNone = 0, kDtDt = 1, kDtComplement = 2, kLogNone = 3, kLogComplement = 4 };
+template <int kMode>
+struct ModeOf {
+    static constexpr bool log = kMode >= kLogNone;
+    static constexpr bool dt = kMode == kDtDt;
+    static constexpr bool complement = kMode == kDtComplement || kMode == kLogComplement;
+};
+
+// Block size: 16 KB of each activation per tile in both types.
+template <typename T>
+struct Threads;
+template <>
+struct Threads<float> { static constexpr int n = 128; };
+template <>
+struct Threads<__nv_bfloat16> { static constexpr int n = 256; };
+
+template <typename T, int kCb>
+struct Tile {
+    static constexpr int nt = Threads<T>::n;
+    static constexpr int lanes = kCb / 2;            // threads per row
+    static constexpr int segs = nt / lanes;          // segments per tile
+    static constexpr int per_warp = 32 / lanes;      // segments per warp
+    static constexpr int warps = nt / 32;
+    static constexpr int tok = segs * kSeg;
+    static constexpr int row = kCb * (int)sizeof(T);  // bytes
+    // a warp's segments start in different banks
+    static constexpr int seg = kSeg * row + (per_warp > 1 ? row : 0);
+    static constexpr int bytes = segs * seg;          // one activation
+};
+
+__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store_pair(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float minus_infinity() { return __uint_as_float(0xFF800000u); }
+
+// q(t) of 1 - exp(-t) = t q(t) for |t| < 1/2 (coefficients from
+// mamba_ssd_sequence_b200/gen_decay_poly.py, relative error 2.1e-7).
+__device__ __forceinline__ float decay_poly(float t) {
+    float p = -1.398218563e-03f;
+    p = fmaf(p, t, 8.408029564e-03f);
+    p = fmaf(p, t, -4.166579247e-02f);
+    p = fmaf(p, t, 1.666596532e-01f);
+    p = fmaf(p, t, -5.000000000e-01f);
+    return fmaf(p, t, 1.000000119e+00f);
+}
+
+// a = exp(-t) and 1 - a.  Near t = 0 the hardware exponential's error (2^-22)
+// would have one sign over the many tokens that a slow decay spans, and add
+// up; 1 - t q(t) is rounded once, either way, and its 1 - a is exact to its
+// last bits.
+__device__ __forceinline__ float decay_of(float t, float *one_minus) {
+    const float w = t * decay_poly(t), e = ptx::ex2_approx(t * -1.4426950408889634f);
+    const bool small = fabsf(t) < 0.5f;
+    *one_minus = small ? w : 1.0f - e;
+    return small ? 1.0f - w : e;
+}
+
+// dt = softplus(p) (softplus_fast of ssd_math.cuh) and d dt / d p = sigmoid(p).
+__device__ __forceinline__ float softplus_slope(float p, float *slope) {
+    const float u = ptx::ex2_approx(-fabsf(p) * 1.4426950408889634f);
+    float q = 5.126102362e-03f;
+    q = fmaf(q, u, -2.907406539e-02f);
+    q = fmaf(q, u, 7.751608640e-02f);
+    q = fmaf(q, u, -1.360224783e-01f);
+    q = fmaf(q, u, 1.907688081e-01f);
+    q = fmaf(q, u, -2.483539879e-01f);
+    q = fmaf(q, u, 3.331812024e-01f);
+    q = fmaf(q, u, -4.999944568e-01f);
+    q = fmaf(q, u, 9.999999404e-01f);
+    *slope = __fdividef(p >= 0.0f ? 1.0f : u, 1.0f + u);
+    return fmaxf(p, 0.0f) + u * q;
+}
+
+// One token of one channel: the decay a, the factor f of x.
+template <int kMode>
+__device__ __forceinline__ float gate_of(float g, float bias, float rate, float *f) {
+    float w, s = 0.0f, t;
+    if (ModeOf<kMode>::log) {
+        t = -g;
+    } else {
+        s = softplus_fast(g + bias);
+        t = rate * s;
+    }
+    const float a = decay_of(t, &w);
+    *f = ModeOf<kMode>::dt ? s : ModeOf<kMode>::complement ? w : 1.0f;
+    return a;
+}
+
+__device__ __forceinline__ int length_of(const int *lengths, int b, int N) {
+    return lengths ? min(max(lengths[b], 0), N) : N;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+__device__ __forceinline__ void st_dsmem_f4(uint32_t cluster_addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Fetches a tile of one activation (base: its token 0, channel 0; tokens from
+// t0, channels from c0) into shared memory.  Places at or behind token `len`
+// or channel `d` receive 0.  Aligned views go through asynchronous 16-byte
+// copies, others element by element.
+template <typename T, int kCb>
+__device__ __forceinline__ void fetch_tile(unsigned char *dst, const T *base, long long stride_n, long long t0, int len,
+                                           int c0, int d, bool aligned) {
+    using Tl = Tile<T, kCb>;
+    if (aligned) {
+        constexpr int vec = 16 / sizeof(T), cpr = kCb / vec, per_thread = Tl::tok * cpr / Tl::nt;
+        const int col = (threadIdx.x % cpr) * vec;
+        const int row0 = threadIdx.x / cpr;
+        const bool cv = c0 + col < d;
+        const uint32_t s0 = ptx::smem_u32(dst) + col * (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < per_thread; ++i) {
+            const int row = row0 + i * (Tl::nt / cpr);
+            const long long t = t0 + row;
+            const bool v = cv && t < len;
+            cp_async16(s0 + (row / kSeg) * Tl::seg + (row % kSeg) * Tl::row,
+                       v ? static_cast<const void *>(base + t * stride_n + c0 + col) : base, v);
+        }
+    } else {
+        for (int e = threadIdx.x; e < Tl::tok * kCb; e += Tl::nt) {
+            const int row = e / kCb, col = e % kCb;
+            const long long t = t0 + row;
+            T v = T(0.0f);
+            if (t < len && c0 + col < d) v = base[t * stride_n + c0 + col];
+            *reinterpret_cast<T *>(dst + (row / kSeg) * Tl::seg + (row % kSeg) * Tl::row + col * (int)sizeof(T)) = v;
+        }
+    }
+}
+
+// The 16-token column pair of this thread in a fetched tile.
+template <typename T, int kCb>
+__device__ __forceinline__ T *own_column(unsigned char *tile) {
+    using Tl = Tile<T, kCb>;
+    return reinterpret_cast<T *>(tile + (threadIdx.x / Tl::lanes) * Tl::seg) + 2 * (threadIdx.x % Tl::lanes);
+}
+
+// Softplus gates of tokens that do not count become -infinity (a = 1, dt = 0);
+// a log-decay of 0, which the fetch left there, means the same.  A thread
+// touches only what it reads itself.
+template <typename T, int kCb>
+__device__ __forceinline__ void close_gates(T *col, int valid) {
+    for (int k = max(valid, 0); k < kSeg; ++k)
+        store_pair(col + k * kCb, make_float2(minus_infinity(), minus_infinity()));
+}
+
+// (A, h) of two channels: the map h_in -> A h_in + h over a span of tokens,
+// as {A0, h0, A1, h1}.  then(p, q): p's span, and q's after it in the
+// direction of the scan.
+__device__ __forceinline__ float4 then(float4 p, float4 q) {
+    return make_float4(p.x * q.x, fmaf(q.x, p.y, q.y), p.z * q.z, fmaf(q.z, p.w, q.w));
+}
+__device__ __forceinline__ float4 identity_map() { return make_float4(1.0f, 0.0f, 1.0f, 0.0f); }
+__device__ __forceinline__ float2 apply(float4 m, float2 h) {
+    return make_float2(fmaf(m.x, h.x, m.y), fmaf(m.z, h.y, m.w));
+}
+template <bool kUp>
+__device__ __forceinline__ float4 shift(float4 m, int n) {
+    float4 r;
+    if (kUp) {
+        r.x = __shfl_up_sync(0xffffffffu, m.x, n), r.y = __shfl_up_sync(0xffffffffu, m.y, n);
+        r.z = __shfl_up_sync(0xffffffffu, m.z, n), r.w = __shfl_up_sync(0xffffffffu, m.w, n);
+    } else {
+        r.x = __shfl_down_sync(0xffffffffu, m.x, n), r.y = __shfl_down_sync(0xffffffffu, m.y, n);
+        r.z = __shfl_down_sync(0xffffffffu, m.z, n), r.w = __shfl_down_sync(0xffffffffu, m.w, n);
+    }
+    return r;
+}
+
+// The state (or, kForward false, the adjoint) that enters this thread's
+// segment, given the segment's own map and the carry that enters the round's
+// first tile (the last one, backwards); the carry is advanced over the whole
+// round.  `warp_maps` is [warps][lanes], `tile_maps` [2][8][lanes] (two
+// rounds' worth: a block may write the next round's while its peers still
+// read this one's).  Every thread of the cluster takes part.
+template <typename T, int kCb, bool kForward>
+__device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, float4 *warp_maps, float4 *tile_maps,
+                                                int round, int rank, int cluster) {
+    using Tl = Tile<T, kCb>;
+    const int lane = threadIdx.x % Tl::lanes, warp = threadIdx.x / 32, in_warp = (threadIdx.x % 32) / Tl::lanes;
+    // the maps of the segments before this one in its warp, and up to it
+    float4 before = identity_map(), upto = own;
+    if (Tl::per_warp > 1) {
+#pragma unroll
+        for (int n = 1; n < Tl::per_warp; n *= 2) {
+            const float4 o = shift<kForward>(upto, n * Tl::lanes);
+            if (kForward ? in_warp >= n : in_warp + n < Tl::per_warp) upto = then(o, upto);
+        }
+        const float4 o = shift<kForward>(upto, Tl::lanes);
+        if (kForward ? in_warp > 0 : in_warp + 1 < Tl::per_warp) before = o;
+    }
+    if (in_warp == (kForward ? Tl::per_warp - 1 : 0)) warp_maps[warp * Tl::lanes + lane] = upto;
+    __syncthreads();
+    float4 base = identity_map();
+#pragma unroll
+    for (int i = 0; i < Tl::warps; ++i) {
+        const int w = kForward ? i : Tl::warps - 1 - i;
+        if (kForward ? w < warp : w > warp) base = then(base, warp_maps[w * Tl::lanes + lane]);
+    }
+    tile_maps += (round & 1) * 8 * Tl::lanes;
+    const bool last = kForward ? (warp == Tl::warps - 1 && in_warp == Tl::per_warp - 1) : (warp == 0 && in_warp == 0);
+    if (last) {
+        const float4 all = then(base, upto);
+        float4 *slot = tile_maps + rank * Tl::lanes + lane;
+        if (cluster == 1) {
+            *slot = all;
+        } else {
+            const uint32_t at = ptx::smem_u32(slot);
+            for (int r = 0; r < cluster; ++r) st_dsmem_f4(ptx::mapa_shared(at, r), all);
+        }
+    }
+    if (cluster == 1) {
+        __syncthreads();
+    } else {
+        cluster_arrive();
+        cluster_wait();
+    }
+    float2 h = carry;
+    for (int i = 0; i < cluster; ++i) {
+        const int r = kForward ? i : cluster - 1 - i;
+        if (r == rank) h = carry;
+        carry = apply(tile_maps[r * Tl::lanes + lane], carry);
+    }
+    return apply(before, apply(base, h));
+}
+
+// How a call is cut up: blocks of cb channels, and `cluster` blocks that share
+// a channel block's sequence, tile by tile.
+struct Cut {
+    int cb, cluster, nblk;
+    long long blocks;
+};
+Cut cut_of(int B, int H, int N, int d, int dtype);
+
+int launch_fwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s);
+int launch_bwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s);
+
+template <typename K>
+int launch_cluster(K kernel, const Args &g, const Cut &p, int threads, size_t smem, cudaStream_t s) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return SSD_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(p.blocks * p.cluster));
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, g) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+}  // namespace glr
+}  // namespace ssd

@@ -1,0 +1,227 @@
+// Gradients of the gated linear recurrence.
+//
+// The tiles, threads and rounds of the forward pass, walked from the last
+// round to the first: the adjoint l_t = dy_t + a_{t+1} l_{t+1} is the same kind
+// of scan in the other direction.  The states that the forward pass saved, one
+// per thread segment, restart h without a second scan, so a round reads x, the
+// gate and dy once and writes dx and dgate once.
+//
+// A thread keeps a and a h_{t-1} of its 16 tokens in registers while the maps
+// of the adjoint are joined; the softplus and its slope are evaluated again
+// afterwards from the tile in shared memory, which costs less than the
+// registers that would hold them.
+//
+// Bound by HBM: 10 bytes an element in bf16, 20 in fp32, and the states (0.25).
+#include "ssd_glr.cuh"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace glr {
+namespace {
+
+constexpr int kStages = 2;
+
+template <typename T, int kCb>
+constexpr size_t smem_bytes() {
+    using Tl = Tile<T, kCb>;
+    return (size_t)kStages * 3 * Tl::bytes + (Tl::warps + 16) * Tl::lanes * sizeof(float4);
+}
+
+template <typename T, int kCb, int kMode>
+__global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g) {
+    using Tl = Tile<T, kCb>;
+    using M = ModeOf<kMode>;
+    extern __shared__ __align__(128) unsigned char sm[];
+    float4 *warp_maps = reinterpret_cast<float4 *>(sm + kStages * 3 * Tl::bytes);
+    float4 *tile_maps = warp_maps + Tl::warps * Tl::lanes;
+
+    uint32_t cluster;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
+    const int rank = (int)ptx::cluster_ctarank();
+    const long long blk = blockIdx.x / cluster;
+    const int c0 = (int)(blk % g.nblk) * kCb;
+    const int h = (int)((blk / g.nblk) % g.H), b = (int)(blk / g.nblk / g.H);
+    const int lane = threadIdx.x % Tl::lanes, seg = threadIdx.x / Tl::lanes, c = c0 + 2 * lane;
+    const bool on0 = c < g.d, on1 = c + 1 < g.d;
+    const int len = length_of(g.lengths, b, g.N);
+
+    const T *x = static_cast<const T *>(g.x.ptr) + b * g.x.stride_b + h * g.x.stride_h;
+    const T *gate = static_cast<const T *>(g.gate.ptr) + b * g.gate.stride_b + h * g.gate.stride_h;
+    const T *dy = static_cast<const T *>(g.dy.ptr) + b * g.dy.stride_b + h * g.dy.stride_h;
+    const long long round_tok = (long long)cluster * Tl::tok;
+    const int rounds = (int)((len + round_tok - 1) / round_tok);
+    const long long chunks = (g.N + kSeg - 1) / kSeg;
+    const float *states = g.states + ((long long)(b * g.H + h) * chunks) * g.d + c;
+    auto first_token = [&](int i) { return (rounds - 1 - i) * round_tok + (long long)rank * Tl::tok; };
+    auto fetch = [&](int i) {
+        if (i < rounds) {
+            unsigned char *st = sm + (i % kStages) * 3 * Tl::bytes;
+            const long long t0 = first_token(i);
+            fetch_tile<T, kCb>(st, x, g.x.stride_n, t0, len, c0, g.d, g.aligned);
+            fetch_tile<T, kCb>(st + Tl::bytes, gate, g.gate.stride_n, t0, len, c0, g.d, g.aligned);
+            fetch_tile<T, kCb>(st + 2 * Tl::bytes, dy, g.dy.stride_n, t0, len, c0, g.d, g.aligned);
+        }
+        cp_async_commit();
+    };
+    auto state_at = [&](int i) {
+        const long long t0 = first_token(i) + seg * kSeg;
+        float2 v = make_float2(0.0f, 0.0f);
+        if (i < rounds && t0 < len) {
+            if (on0) v.x = states[t0 / kSeg * g.d];
+            if (on1) v.y = states[t0 / kSeg * g.d + 1];
+        }
+        return v;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    float2 next_state = state_at(0);
+
+    float2 rate = make_float2(1.0f, 1.0f), bias = make_float2(0.0f, 0.0f), carry = make_float2(0.0f, 0.0f);
+    const long long pc = (long long)h * g.d + c, bc = (long long)b * g.H * g.d + pc;
+    if (!M::log) {
+        if (g.A_log) rate = make_float2(on0 ? expf(g.A_log[pc]) : 1.0f, on1 ? expf(g.A_log[pc + 1]) : 1.0f);
+        if (g.dt_bias) bias = make_float2(on0 ? g.dt_bias[pc] : 0.0f, on1 ? g.dt_bias[pc + 1] : 0.0f);
+    }
+    if (g.dh_out) carry = make_float2(on0 ? g.dh_out[bc] : 0.0f, on1 ? g.dh_out[bc + 1] : 0.0f);
+
+    T *dx = static_cast<T *>(g.dx.ptr) + b * g.dx.stride_b + h * g.dx.stride_h + c;
+    T *dgate = static_cast<T *>(g.dgate.ptr) + b * g.dgate.stride_b + h * g.dgate.stride_h + c;
+    auto store = [&](T *o, float2 v) {
+        if (g.aligned) {
+            if (on0) store_pair(o, v);
+        } else {
+            if (on0) store_one(o, v.x);
+            if (on1) store_one(o + 1, v.y);
+        }
+    };
+    float2 sumA = make_float2(0.0f, 0.0f), sumb = make_float2(0.0f, 0.0f);
+
+    for (int i = 0; i < rounds; ++i) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();  // this round has arrived for every thread, and the one before it is consumed
+        fetch(i + kStages - 1);
+        unsigned char *st = sm + (i % kStages) * 3 * Tl::bytes;
+        const T *xc = own_column<T, kCb>(st);
+        T *gc = own_column<T, kCb>(st + Tl::bytes);
+        const T *yc = own_column<T, kCb>(st + 2 * Tl::bytes);
+        const long long t0 = first_token(i) + seg * kSeg;
+        const int valid = (int)max(0ll, min((long long)kSeg, len - t0));
+        if (!M::log && valid < kSeg) close_gates<T, kCb>(gc, valid);
+        float2 hs = next_state;
+        next_state = state_at(i + 1);
+        // a, and q = a h_{t-1} (a (h_{t-1} - x) for f = 1 - a): d log a = l q
+        float2 a[kSeg], q[kSeg];
+        float4 own = identity_map();  // l entering the segment -> a_0 l_0
+#pragma unroll
+        for (int k = 0; k < kSeg; ++k) {
+            const float2 xv = load_pair(xc + k * kCb), gv = load_pair(gc + k * kCb), yv = load_pair(yc + k * kCb);
+            float2 f;
+            a[k].x = gate_of<kMode>(gv.x, bias.x, rate.x, &f.x);
+            a[k].y = gate_of<kMode>(gv.y, bias.y, rate.y, &f.y);
+            const float2 ah = make_float2(a[k].x * hs.x, a[k].y * hs.y);
+            q[k] = M::complement ? make_float2(fmaf(-a[k].x, xv.x, ah.x), fmaf(-a[k].y, xv.y, ah.y)) : ah;
+            hs = make_float2(fmaf(f.x, xv.x, ah.x), fmaf(f.y, xv.y, ah.y));
+            own.x *= a[k].x, own.z *= a[k].y;
+            own.y = fmaf(own.x, yv.x, own.y), own.w = fmaf(own.z, yv.y, own.w);
+        }
+        float2 lc = enter_segment<T, kCb, false>(own, carry, warp_maps, tile_maps, i, rank, (int)cluster);
+        float2 segA = make_float2(0.0f, 0.0f), segb = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = kSeg - 1; k >= 0; --k) {
+            const float2 yv = load_pair(yc + k * kCb), gv = load_pair(gc + k * kCb), xv = load_pair(xc + k * kCb);
+            float2 vx, vg;
+            auto channel = [&](float y, float gt, float xx, float av, float qv, float bs, float rt, float &lcar, float &sA,
+                               float &sb, float &ox, float &og) {
+                const float l = lcar + y;
+                lcar = av * l;
+                const float dla = l * qv;
+                float f = 1.0f;
+                if (M::log) {
+                    og = dla;
+                    if (M::complement) (void)decay_of(-gt, &f);
+                } else {
+                    float slope;
+                    const float s = softplus_slope(gt + bs, &slope), t = rt * s;
+                    if (M::complement) f = fabsf(t) < 0.5f ? t * decay_poly(t) : 1.0f - av;
+                    if (M::dt) f = s;
+                    float ds = -rt * dla;
+                    if (M::dt) ds = fmaf(l, xx, ds);
+                    og = ds * slope;
+                    // where a = 0 log a may be -infinity, and the product is 0
+                    sA = fmaf(dla, fmaxf(-t, -200.0f), sA);
+                    sb += og;
+                }
+                ox = f * l;
+            };
+            channel(yv.x, gv.x, xv.x, a[k].x, q[k].x, bias.x, rate.x, lc.x, segA.x, segb.x, vx.x, vg.x);
+            channel(yv.y, gv.y, xv.y, a[k].y, q[k].y, bias.y, rate.y, lc.y, segA.y, segb.y, vx.y, vg.y);
+            const long long t = t0 + k;
+            if (k >= valid) vx = vg = make_float2(0.0f, 0.0f);
+            if (t < g.N) {
+                store(dx + t * g.dx.stride_n, vx);
+                store(dgate + t * g.dgate.stride_n, vg);
+            }
+        }
+        sumA = make_float2(sumA.x + segA.x, sumA.y + segA.y);
+        sumb = make_float2(sumb.x + segb.x, sumb.y + segb.y);
+    }
+    cp_async_wait<0>();
+
+    // whole rounds behind the length
+    for (long long t = rounds * round_tok + (long long)rank * Tl::tok + seg * kSeg; t < g.N; t += round_tok)
+        for (int k = 0; k < kSeg && t + k < g.N; ++k) {
+            store(dx + (t + k) * g.dx.stride_n, make_float2(0.0f, 0.0f));
+            store(dgate + (t + k) * g.dgate.stride_n, make_float2(0.0f, 0.0f));
+        }
+    if (g.dh0 && rank == 0 && seg == 0) {
+        if (on0) g.dh0[bc] = carry.x;
+        if (on1) g.dh0[bc + 1] = carry.y;
+    }
+    // the block's sums of dA_log and ddt_bias, segment by segment
+    if (!M::log && g.part) {
+        __syncthreads();
+        float4 *sums = reinterpret_cast<float4 *>(sm);
+        sums[threadIdx.x] = make_float4(sumA.x, sumb.x, sumA.y, sumb.y);
+        __syncthreads();
+        if (seg == 0) {
+            float4 v = sums[lane];
+            for (int k = 1; k < Tl::segs; ++k) {
+                const float4 o = sums[k * Tl::lanes + lane];
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            float2 *part = reinterpret_cast<float2 *>(g.part) + ((long long)b * cluster + rank) * g.H * g.d + pc;
+            if (on0) part[0] = make_float2(v.x, v.y);
+            if (on1) part[1] = make_float2(v.z, v.w);
+        }
+    }
+    // no block leaves while a peer may still write to its shared memory
+    if (cluster > 1) ptx::cluster_sync_all();
+}
+
+template <typename T, int kCb>
+int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
+    constexpr size_t sm = smem_bytes<T, kCb>();
+    constexpr int nt = Threads<T>::n;
+    switch (mode) {
+    case kDtNone: return launch_cluster(glr_bwd_kernel<T, kCb, kDtNone>, g, p, nt, sm, s);
+    case kDtDt: return launch_cluster(glr_bwd_kernel<T, kCb, kDtDt>, g, p, nt, sm, s);
+    case kDtComplement: return launch_cluster(glr_bwd_kernel<T, kCb, kDtComplement>, g, p, nt, sm, s);
+    case kLogNone: return launch_cluster(glr_bwd_kernel<T, kCb, kLogNone>, g, p, nt, sm, s);
+    default: return launch_cluster(glr_bwd_kernel<T, kCb, kLogComplement>, g, p, nt, sm, s);
+    }
+}
+
+template <typename T>
+int launch_cb(const Args &g, const Cut &p, int mode, cudaStream_t s) {
+    return p.cb == 64 ? launch_mode<T, 64>(g, p, mode, s)
+                      : p.cb == 32 ? launch_mode<T, 32>(g, p, mode, s) : launch_mode<T, 16>(g, p, mode, s);
+}
+
+}  // namespace
+
+int launch_bwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s) {
+    return dtype == SSD_F32 ? launch_cb<float>(g, p, mode, s) : launch_cb<__nv_bfloat16>(g, p, mode, s);
+}
+
+}  // namespace glr
+}  // namespace ssd

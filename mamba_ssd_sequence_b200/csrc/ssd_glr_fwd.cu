@@ -1,0 +1,160 @@
+// Forward pass of the gated linear recurrence h_t = a_t h_{t-1} + f_t x_t.
+//
+// A cluster takes one block of channels through its sequence in rounds of
+// cluster x tile tokens.  In a round each thread evaluates the gates of its
+// 16-token segment once, keeps a and f x in registers, and reduces them to the
+// segment's map h_in -> A h_in + h; the maps are joined over the segments of a
+// warp (shuffles), the warps of a block (shared memory) and the blocks of the
+// cluster (distributed shared memory), which gives each segment its h_in; a
+// second walk over the registers then gives h.  So x and the gate are read and
+// h is written once, whatever the number of channels.
+//
+// Bound by HBM: 6 bytes an element in bf16, 12 in fp32.
+#include "ssd_glr.cuh"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace glr {
+namespace {
+
+constexpr int kStages = 3;
+
+template <typename T, int kCb>
+constexpr size_t smem_bytes() {
+    using Tl = Tile<T, kCb>;
+    return (size_t)kStages * 2 * Tl::bytes + (Tl::warps + 16) * Tl::lanes * sizeof(float4);
+}
+
+template <typename T, int kCb, int kMode>
+__global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g) {
+    using Tl = Tile<T, kCb>;
+    using M = ModeOf<kMode>;
+    extern __shared__ __align__(128) unsigned char sm[];
+    float4 *warp_maps = reinterpret_cast<float4 *>(sm + kStages * 2 * Tl::bytes);
+    float4 *tile_maps = warp_maps + Tl::warps * Tl::lanes;
+
+    uint32_t cluster;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
+    const int rank = (int)ptx::cluster_ctarank();
+    const long long blk = blockIdx.x / cluster;
+    const int c0 = (int)(blk % g.nblk) * kCb;
+    const int h = (int)((blk / g.nblk) % g.H), b = (int)(blk / g.nblk / g.H);
+    const int seg = threadIdx.x / Tl::lanes, c = c0 + 2 * (threadIdx.x % Tl::lanes);
+    const bool on0 = c < g.d, on1 = c + 1 < g.d;
+    const int len = length_of(g.lengths, b, g.N);
+
+    const T *x = static_cast<const T *>(g.x.ptr) + b * g.x.stride_b + h * g.x.stride_h;
+    const T *gate = static_cast<const T *>(g.gate.ptr) + b * g.gate.stride_b + h * g.gate.stride_h;
+    const long long round_tok = (long long)cluster * Tl::tok;
+    const int rounds = (int)((len + round_tok - 1) / round_tok);
+    auto fetch = [&](int r) {
+        if (r < rounds) {
+            unsigned char *st = sm + (r % kStages) * 2 * Tl::bytes;
+            const long long t0 = r * round_tok + (long long)rank * Tl::tok;
+            fetch_tile<T, kCb>(st, x, g.x.stride_n, t0, len, c0, g.d, g.aligned);
+            fetch_tile<T, kCb>(st + Tl::bytes, gate, g.gate.stride_n, t0, len, c0, g.d, g.aligned);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int r = 0; r < kStages - 1; ++r) fetch(r);
+
+    float2 rate = make_float2(1.0f, 1.0f), bias = make_float2(0.0f, 0.0f), carry = make_float2(0.0f, 0.0f);
+    const long long pc = (long long)h * g.d + c, bc = (long long)b * g.H * g.d + pc;
+    if (!M::log) {
+        if (g.A_log) rate = make_float2(on0 ? expf(g.A_log[pc]) : 1.0f, on1 ? expf(g.A_log[pc + 1]) : 1.0f);
+        if (g.dt_bias) bias = make_float2(on0 ? g.dt_bias[pc] : 0.0f, on1 ? g.dt_bias[pc + 1] : 0.0f);
+    }
+    if (g.h0) carry = make_float2(on0 ? g.h0[bc] : 0.0f, on1 ? g.h0[bc + 1] : 0.0f);
+
+    T *out = static_cast<T *>(g.out.ptr) + b * g.out.stride_b + h * g.out.stride_h + c;
+    const long long chunks = (g.N + kSeg - 1) / kSeg;
+    float *states = g.states ? g.states + ((long long)(b * g.H + h) * chunks) * g.d + c : nullptr;
+    auto store = [&](long long t, float2 v) {
+        T *o = out + t * g.out.stride_n;
+        if (g.aligned) {
+            if (on0) store_pair(o, v);
+        } else {
+            if (on0) store_one(o, v.x);
+            if (on1) store_one(o + 1, v.y);
+        }
+    };
+    auto save = [&](long long chunk, float2 v) {
+        if (on0) states[chunk * g.d] = v.x;
+        if (on1) states[chunk * g.d + 1] = v.y;
+    };
+
+    for (int r = 0; r < rounds; ++r) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();  // round r has arrived for every thread, and round r - 1 is consumed
+        fetch(r + kStages - 1);
+        unsigned char *st = sm + (r % kStages) * 2 * Tl::bytes;
+        const T *xc = own_column<T, kCb>(st);
+        T *gc = own_column<T, kCb>(st + Tl::bytes);
+        const long long t0 = r * round_tok + (long long)rank * Tl::tok + seg * kSeg;
+        const int valid = (int)max(0ll, min((long long)kSeg, len - t0));
+        if (!M::log && valid < kSeg) close_gates<T, kCb>(gc, valid);
+        float2 a[kSeg], u[kSeg];
+        float4 own = identity_map();
+#pragma unroll
+        for (int k = 0; k < kSeg; ++k) {
+            const float2 xv = load_pair(xc + k * kCb), gv = load_pair(gc + k * kCb);
+            float2 f;
+            a[k].x = gate_of<kMode>(gv.x, bias.x, rate.x, &f.x);
+            a[k].y = gate_of<kMode>(gv.y, bias.y, rate.y, &f.y);
+            u[k] = make_float2(f.x * xv.x, f.y * xv.y);
+            own = then(own, make_float4(a[k].x, u[k].x, a[k].y, u[k].y));
+        }
+        float2 hs = enter_segment<T, kCb, true>(own, carry, warp_maps, tile_maps, r, rank, (int)cluster);
+        if (states && t0 < g.N) save(t0 / kSeg, hs);
+#pragma unroll
+        for (int k = 0; k < kSeg; ++k) {
+            hs = make_float2(fmaf(a[k].x, hs.x, u[k].x), fmaf(a[k].y, hs.y, u[k].y));
+            if (k < valid)
+                store(t0 + k, hs);
+            else if (t0 + k < g.N)
+                store(t0 + k, make_float2(0.0f, 0.0f));
+        }
+    }
+    cp_async_wait<0>();
+
+    // whole rounds behind the length
+    for (long long t = rounds * round_tok + (long long)rank * Tl::tok + seg * kSeg; t < g.N; t += round_tok) {
+        if (states) save(t / kSeg, carry);
+        for (int k = 0; k < kSeg && t + k < g.N; ++k) store(t + k, make_float2(0.0f, 0.0f));
+    }
+    if (g.h_out && rank == 0 && seg == 0) {
+        if (on0) g.h_out[bc] = carry.x;
+        if (on1) g.h_out[bc + 1] = carry.y;
+    }
+    // no block leaves while a peer may still write to its shared memory
+    if (cluster > 1) ptx::cluster_sync_all();
+}
+
+template <typename T, int kCb>
+int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
+    constexpr size_t sm = smem_bytes<T, kCb>();
+    constexpr int nt = Threads<T>::n;
+    switch (mode) {
+    case kDtNone: return launch_cluster(glr_fwd_kernel<T, kCb, kDtNone>, g, p, nt, sm, s);
+    case kDtDt: return launch_cluster(glr_fwd_kernel<T, kCb, kDtDt>, g, p, nt, sm, s);
+    case kDtComplement: return launch_cluster(glr_fwd_kernel<T, kCb, kDtComplement>, g, p, nt, sm, s);
+    case kLogNone: return launch_cluster(glr_fwd_kernel<T, kCb, kLogNone>, g, p, nt, sm, s);
+    default: return launch_cluster(glr_fwd_kernel<T, kCb, kLogComplement>, g, p, nt, sm, s);
+    }
+}
+
+template <typename T>
+int launch_cb(const Args &g, const Cut &p, int mode, cudaStream_t s) {
+    return p.cb == 64 ? launch_mode<T, 64>(g, p, mode, s)
+                      : p.cb == 32 ? launch_mode<T, 32>(g, p, mode, s) : launch_mode<T, 16>(g, p, mode, s);
+}
+
+}  // namespace
+
+int launch_fwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s) {
+    return dtype == SSD_F32 ? launch_cb<float>(g, p, mode, s) : launch_cb<__nv_bfloat16>(g, p, mode, s);
+}
+
+}  // namespace glr
+}  // namespace ssd

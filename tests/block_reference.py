@@ -6,6 +6,11 @@ one float32 rounding.  Of the recurrence, per token:
   log a   softplus (polynomial and hardware base-2 exponential: 5 U), the rate
           exp(A_log) (3 U) and their product (1 U): 9 U relative, so a is off
           by 9 U |log a| relative, and by 3 U from its own evaluation;
+  p       gate + dt_bias is rounded once and scaled once inside the exponential,
+          so p is off by 2 U |p|, which changes dt by 2 k U relative with
+          k = |p| sigmoid(p) / softplus(p) (the logarithmic derivative of the
+          softplus times |p|; for p = -14, k = 14), and its slope sigmoid(p)
+          by 2 |p| (1 - sigmoid(p)) U relative;
   f       9 U relative for dt; 1 - a = -expm1(log a) is off by at most
           (9 + 3) U relative, since |log a| a / (1 - a) <= 1; f x: 1 U more;
   h       1 U for the multiply-add, 1 U for the running product of decays
@@ -56,6 +61,16 @@ def recurrence(x, gate, A_log=None, dt_bias=None, h0=None, lengths=None, kind="d
     a = torch.where(live, a, one)
     f, x_ = torch.where(live, f, 0 * one), torch.where(live, x, 0 * one)
     lam_ = torch.where(live, la.clamp(min=-200.0), 0 * one).abs()
+    if kind == "log":
+        k2, s2 = 0 * one, 0 * one
+    else:  # 2 k and 2 |p| (1 - sigmoid(p)) of the roundings of p
+        p = gate if dt_bias is None else gate + dt_bias.view(1, H, 1, d)
+        fin = torch.isfinite(p) & live
+        p = torch.where(fin, p, 0 * one)
+        k2 = torch.where(fin, 2 * p.abs() * torch.sigmoid(p) / torch.nn.functional.softplus(p), 0 * one)
+        s2 = torch.where(fin, 2 * p.abs() * torch.sigmoid(-p), 0 * one)
+    nla, kf = (9 + k2) * lam_, k2 if value != "none" else 0 * k2  # |log a|'s error, f's share of it
+    nla, kf = nla.expand(B, H, N, d), kf.expand(B, H, N, d)
     u = f * x_
     h = zero.clone() if h0 is None else h0.clone()
     env, err = h.abs(), zero.clone()
@@ -65,7 +80,7 @@ def recurrence(x, gate, A_log=None, dt_bias=None, h0=None, lengths=None, kind="d
         at = a[:, :, t]
         g = at * env
         h = at * h + u[:, :, t]
-        err = at * err + U * ((9 * lam_[:, :, t] + 5) * g + 13 * u[:, :, t].abs())
+        err = at * err + U * ((nla[:, :, t] + 5) * g + (13 + kf[:, :, t]) * u[:, :, t].abs())
         env = g + u[:, :, t].abs()
         err = torch.where(live[:, :, t], err + U * env, err)
         ys.append(h), yt.append(err)
@@ -84,15 +99,15 @@ def recurrence(x, gate, A_log=None, dt_bias=None, h0=None, lengths=None, kind="d
         lerr = lerr + 2 * U * lenv
         L[t], LE[t], LR[t] = lam, lenv, lerr
         at = a[:, :, t]
-        lerr = at * (lerr + U * torch.where(live[:, :, t], 9 * lam_[:, :, t] + 5, 0 * one) * lenv)
+        lerr = at * (lerr + U * torch.where(live[:, :, t], nla[:, :, t] + 5, 0 * one) * lenv)
         lam, lenv = at * lam, at * lenv
     out["dh0"], out["dh0_tol"] = lam, lerr
     L, LE, LR = (torch.stack(v, 2) for v in (L, LE, LR))
-    out["dx"], out["dx_tol"] = f * L, f.abs() * (LR + 14 * U * LE)
-    dla, dla_t = a * L * before, a * (LR * env_b + LE * err_b + U * (9 * lam_ + 8) * LE * env_b)
+    out["dx"], out["dx_tol"] = f * L, f.abs() * (LR + (14 + kf) * U * LE)
+    dla, dla_t = a * L * before, a * (LR * env_b + LE * err_b + U * (nla + 8) * LE * env_b)
     if value == "complement":
         dla = dla - a * L * x_
-        dla_t = dla_t + a * x_.abs() * (LR + U * (9 * lam_ + 8) * LE) + U * (a * LE * (env_b + x_.abs()))
+        dla_t = dla_t + a * x_.abs() * (LR + U * (nla + 8) * LE) + U * (a * LE * (env_b + x_.abs()))
     dla, dla_t = torch.where(live, dla, 0 * one), torch.where(live, dla_t, 0 * one)
     if kind == "log":
         out["dgate"], out["dgate_tol"] = dla, dla_t
@@ -102,10 +117,10 @@ def recurrence(x, gate, A_log=None, dt_bias=None, h0=None, lengths=None, kind="d
         ds, ds_t, mag = ds + L * x_, ds_t + x_.abs() * (LR + 2 * U * LE), mag + LE * x_.abs()
     sg = torch.where(live, sg, 0 * one)
     # the sigmoid: exponential, sum, quotient, each product: 8 U
-    out["dgate"], out["dgate_tol"] = ds * sg, sg * (ds_t + 8 * U * mag)
+    out["dgate"], out["dgate_tol"] = ds * sg, sg * (ds_t + (8 + s2) * U * mag)
     n = N + B + 8  # no chain of additions is longer
     la0 = torch.where(live, la.clamp(min=-200.0), 0 * one)
-    for name, term, tol in (("dA_log", dla * la0, lam_ * (dla_t + 12 * U * a * LE * (env_b + x_.abs()))),
+    for name, term, tol in (("dA_log", dla * la0, lam_ * (dla_t + (12 + k2) * U * a * LE * (env_b + x_.abs()))),
                             ("ddt_bias", out["dgate"], out["dgate_tol"])):
         out[name] = term.sum((0, 2)).reshape(-1)
         out[name + "_tol"] = (tol.sum((0, 2)) + n * U * (term.abs() + tol).sum((0, 2))).reshape(-1)

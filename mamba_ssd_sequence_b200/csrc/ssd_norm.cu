@@ -2,21 +2,25 @@
 // a root-mean-square norm, the gated root-mean-square norm behind the
 // operator, and their gradients.
 //
-// A block walks the rows (a token, or a token's group of channels) of one
-// slab; a thread always meets the same channels, so the gradients of the
-// per-channel parameters are summed by one thread each over the slab's rows,
-// and then over the slabs in order.
+// A row (a token, or a token's group of channels) stays in the registers of
+// `tpr` threads, kNv vectors of kVec channels each, from its one load to its
+// one store.  A thread meets the same channels in every row, so the gradients
+// of per-channel parameters are sums in registers, joined over a block's rows
+// in shared memory and over the blocks by a second kernel, in a fixed order.
+// Bound by HBM.
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include "ptx.cuh"
 #include "ssd_internal.h"
 #include "ssd_view.h"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a block, unless a row takes more
 
+// ------------------------------------------------------------ vectors of a row
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
@@ -26,6 +30,466 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// 16 bytes of a type
+template <typename T>
+constexpr int kVecOf = 16 / (int)sizeof(T);
+
+template <int kVec>
+__device__ __forceinline__ void load16(const float *p, float (&v)[kVec]) {
+#pragma unroll
+    for (int i = 0; i < kVec; i += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p + i);
+        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+    }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+template <int kVec>
+__device__ __forceinline__ void store16(float *p, const float (&v)[kVec]) {
+#pragma unroll
+    for (int i = 0; i < kVec; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A vector of a row, `left` channels before the row's end (the rest reads 0).
+// Rows, views and parameters that are not 16-byte aligned go channel by channel;
+// a thread holds the same channels either way, so the sums have the same bits.
+template <bool kAligned, typename T, int kVec>
+__device__ __forceinline__ void load(const T *p, int left, float (&v)[kVec]) {
+    if constexpr (kAligned) {
+        load16(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] = e < left ? to_f32(p[e]) : 0.0f;
+    }
+}
+template <bool kAligned, typename T, int kVec>
+__device__ __forceinline__ void store(T *p, int left, const float (&v)[kVec]) {
+    if constexpr (kAligned) {
+        store16(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (e < left) p[e] = from_f32<T>(v[e]);
+    }
+}
+template <bool kAligned, int kVec>
+__device__ __forceinline__ void load_param(const float *p, int c, int left, float otherwise, float (&v)[kVec]) {
+    if (p) {
+        load<kAligned>(p + c, left, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = otherwise;
+    }
+}
+
+// Sum over a row's `tpr` threads (a power of two), the same bits in each.
+// Rows of more than a warp meet in `red` ([2][32], by the parity of `turn`, so
+// that one barrier a row is enough); every thread of the block calls this.
+__device__ __forceinline__ float row_sum(float v, int tpr, float (*red)[32], int turn) {
+    for (int o = min(tpr, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tpr <= 32) return v;
+    float *r = red[turn & 1];
+    const int warp = threadIdx.x / 32, per_row = tpr / 32, first = warp / per_row * per_row;
+    if (threadIdx.x % 32 == 0) r[warp] = v;
+    __syncthreads();
+    float s = r[first];
+    for (int i = 1; i < per_row; ++i) s += r[first + i];
+    return s;
+}
+
+// Joins the block's rows' sums of a per-channel gradient and writes them to
+// the block's place.  `acc` is [kNv][kVec] of each thread; the rows that share
+// channels are `rows` threads' worth of tpr apart by `step`.
+template <int kNv, int kVec>
+__device__ __forceinline__ void write_part(const float (&acc)[kNv][kVec], float *sh, int slot, int slots, int lane,
+                                           int tpr, int same, int L, float *part) {
+    // slots s, s + same, s + 2 same, ... hold the same channels
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kNv; ++i)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sh[(i * kVec + e) * blockDim.x + threadIdx.x] = acc[i][e];
+    __syncthreads();
+    if (slot < same) {
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int c = (lane + i * tpr) * kVec;
+            if (c < L) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float *p = sh + (i * kVec + e) * blockDim.x + threadIdx.x;
+                    float s = p[0];
+                    for (int k = same; k < slots; k += same) s += p[k * tpr];
+                    if (c + e < L) part[c + e] = s;
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ T *row_of(const ssd_rows &v, long long m) {
+    return v.ptr ? static_cast<T *>(v.ptr) + m * v.stride : nullptr;
+}
+
+// ------------------------------------------------------- residual add and norm
+struct AddNormArgs {
+    ssd_rows x, res, r, out, dy, dres, dr, dx;
+    const float *scale, *w;
+    float *rstd, *part;
+    int M, C, tpr, want_scale;
+    float eps;
+};
+
+template <typename T, typename R, bool kAligned, int kNv, int kMax>
+__global__ void __launch_bounds__(kMax) add_norm_kernel(const AddNormArgs g) {
+    constexpr int kVec = kVecOf<T>;
+    __shared__ float red[2][32];
+    const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr;
+    int turn = 0;
+    for (long long m0 = (long long)blockIdx.x * slots; m0 < g.M; m0 += (long long)gridDim.x * slots, ++turn) {
+        const long long m = m0 + slot;
+        const bool on = m < g.M;
+        const T *x = row_of<const T>(g.x, on ? m : 0);
+        const R *res = row_of<const R>(g.res, on ? m : 0);
+        float v[kNv][kVec], ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int c = (lane + i * tpr) * kVec;
+            if (on && c < g.C) {
+                load<kAligned>(x + c, g.C - c, v[i]);
+                // the product and the sum are rounded one after the other, as
+                // two operations on the stream are
+                if (g.scale) {
+                    float sc[kVec];
+                    load_param<kAligned>(g.scale, c, g.C - c, 1.0f, sc);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) v[i][e] = __fmul_rn(sc[e], v[i][e]);
+                }
+                if (res) {
+                    float q[kVec];
+                    load<kAligned>(res + c, g.C - c, q);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) v[i][e] = __fadd_rn(q[e], v[i][e]);
+                }
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    v[i][e] = to_f32(from_f32<R>(v[i][e]));
+                    ss = fmaf(v[i][e], v[i][e], ss);
+                }
+            }
+        }
+        const float rs = rsqrtf(row_sum(ss, tpr, red, turn) / g.C + g.eps);
+        if (!on) continue;
+        R *r = row_of<R>(g.r, m);
+        T *out = row_of<T>(g.out, m);
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int c = (lane + i * tpr) * kVec;
+            if (c < g.C) {
+                if (r) store<kAligned>(r + c, g.C - c, v[i]);
+                float w[kVec];
+                load_param<kAligned>(g.w, c, g.C - c, 1.0f, w);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) v[i][e] = v[i][e] * rs * w[e];
+                store<kAligned>(out + c, g.C - c, v[i]);
+            }
+        }
+        if (g.rstd && lane == 0) g.rstd[m] = rs;
+    }
+}
+
+template <typename T, typename R, bool kAligned, int kNv, int kMax>
+__global__ void __launch_bounds__(kMax) add_norm_bwd_kernel(const AddNormArgs g) {
+    constexpr int kVec = kVecOf<T>;
+    extern __shared__ float sh[];
+    __shared__ float red[2][32];
+    const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr;
+    float dw[kNv][kVec] = {}, dsc[kNv][kVec] = {};
+    int turn = 0;
+    for (long long m0 = (long long)blockIdx.x * slots; m0 < g.M; m0 += (long long)gridDim.x * slots, ++turn) {
+        const long long m = m0 + slot;
+        const bool on = m < g.M;
+        const R *r = row_of<const R>(g.r, on ? m : 0);
+        const T *dy = row_of<const T>(g.dy, on ? m : 0);
+        const float rs = on ? g.rstd[m] : 0.0f;
+        float xh[kNv][kVec], gy[kNv][kVec], dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int c = (lane + i * tpr) * kVec;
+            if (on && c < g.C) {
+                load<kAligned>(r + c, g.C - c, xh[i]);
+                load<kAligned>(dy + c, g.C - c, gy[i]);
+                float w[kVec];
+                load_param<kAligned>(g.w, c, g.C - c, 1.0f, w);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    xh[i][e] *= rs;
+                    dw[i][e] = fmaf(gy[i][e], xh[i][e], dw[i][e]);
+                    gy[i][e] *= w[e];
+                    dot = fmaf(gy[i][e], xh[i][e], dot);
+                }
+            }
+        }
+        dot = row_sum(dot, tpr, red, turn) / g.C;
+        if (!on) continue;
+        const T *x = row_of<const T>(g.x, m);
+        const R *dres = row_of<const R>(g.dres, m);
+        R *dr = row_of<R>(g.dr, m);
+        T *dx = row_of<T>(g.dx, m);
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int c = (lane + i * tpr) * kVec;
+            if (c < g.C) {
+                float q[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) gy[i][e] = rs * fmaf(-xh[i][e], dot, gy[i][e]);
+                if (dres) {
+                    load<kAligned>(dres + c, g.C - c, q);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) gy[i][e] += q[e];
+                }
+                store<kAligned>(dr + c, g.C - c, gy[i]);
+                if (x) {
+                    load<kAligned>(x + c, g.C - c, q);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) dsc[i][e] = fmaf(gy[i][e], q[e], dsc[i][e]);
+                }
+                if (dx) {
+                    load_param<kAligned>(g.scale, c, g.C - c, 1.0f, q);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) q[e] *= gy[i][e];
+                    store<kAligned>(dx + c, g.C - c, q);
+                }
+            }
+        }
+    }
+    if (g.part) {
+        float *part = g.part + (long long)blockIdx.x * 2 * g.C;
+        write_part<kNv, kVec>(dw, sh, slot, slots, lane, tpr, 1, g.C, part);
+        if (g.want_scale) write_part<kNv, kVec>(dsc, sh, slot, slots, lane, tpr, 1, g.C, part + g.C);
+    }
+}
+
+// Sums of the blocks' partial rows, in order: 32 channels and 8 interleaved
+// ranges of rows a block.  outs[blockIdx.y] takes the sums of part + blockIdx.y C.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float *part, int rows, long long stride, int C, float *out0,
+                                                        float *out1) {
+    __shared__ float red[8][32];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
+    float *out = blockIdx.y ? out1 : out0;
+    part += (long long)blockIdx.y * C;
+    float s = 0.0f;
+    ptx::pdl_wait();
+    if (c < C && out) {
+#pragma unroll 8
+        for (int i = k; i < rows; i += 8) s += part[i * stride + c];
+    }
+    red[k][threadIdx.x % 32] = s;
+    __syncthreads();
+    if (k == 0 && c < C && out) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
+        out[c] = s;
+    }
+}
+
+// ------------------------------------------------------------------ gated norm
+struct GatedNormArgs {
+    ssd_view x, z, out, dy, dx, dz;
+    const float *w;
+    float *rstd, *part;
+    int B, H, N, d, groups, gpb, L, tpr, after;
+    float eps;
+};
+
+// A vector of a token's channels from place j of head h on; unaligned vectors
+// may run into the next head.
+template <bool kAligned, typename T, int kVec>
+__device__ __forceinline__ void load_heads(const T *p, long long stride_h, int h, int j, int d, int left,
+                                           float (&v)[kVec]) {
+    p += h * stride_h + j;
+    if constexpr (kAligned) {
+        load16(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            v[e] = e < left ? to_f32(*p) : 0.0f;
+            ++p;
+            if (++j == d) j = 0, p += stride_h - d;
+        }
+    }
+}
+template <bool kAligned, typename T, int kVec>
+__device__ __forceinline__ void store_heads(T *p, long long stride_h, int h, int j, int d, int left,
+                                            const float (&v)[kVec]) {
+    p += h * stride_h + j;
+    if constexpr (kAligned) {
+        store16(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            if (e < left) *p = from_f32<T>(v[e]);
+            ++p;
+            if (++j == d) j = 0, p += stride_h - d;
+        }
+    }
+}
+
+template <typename T, bool kAligned, int kNv, int kMax>
+__global__ void __launch_bounds__(kMax) gated_norm_kernel(const GatedNormArgs g) {
+    constexpr int kVec = kVecOf<T>;
+    __shared__ float red[2][32];
+    const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr / g.gpb;
+    const int group = blockIdx.y * g.gpb + slot % g.gpb, c0 = group * g.L;
+    const long long tokens = (long long)g.B * g.N;
+    int turn = 0;
+    for (long long m0 = (long long)blockIdx.x * slots; m0 < tokens; m0 += (long long)gridDim.x * slots, ++turn) {
+        const long long m = m0 + slot / g.gpb;
+        const bool on = m < tokens;
+        const long long b = on ? m / g.N : 0, n = on ? m % g.N : 0;
+        const T *x = static_cast<const T *>(g.x.ptr) + b * g.x.stride_b + n * g.x.stride_n;
+        const T *z = g.z.ptr ? static_cast<const T *>(g.z.ptr) + b * g.z.stride_b + n * g.z.stride_n : nullptr;
+        float v[kNv][kVec], s[kNv][kVec], ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int cl = (lane + i * tpr) * kVec;
+            if (on && cl < g.L) {
+                const int c = c0 + cl, h = c / g.d, j = c % g.d;
+                load_heads<kAligned>(x, g.x.stride_h, h, j, g.d, g.L - cl, v[i]);
+                if (z) {
+                    load_heads<kAligned>(z, g.z.stride_h, h, j, g.d, g.L - cl, s[i]);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) s[i][e] = __fdividef(s[i][e], 1.0f + expf(-s[i][e]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) s[i][e] = 1.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float u = g.after ? v[i][e] : v[i][e] * s[i][e];
+                    ss = fmaf(u, u, ss);
+                    v[i][e] *= s[i][e];
+                }
+            }
+        }
+        const float rs = rsqrtf(row_sum(ss, tpr, red, turn) / g.L + g.eps);
+        if (!on) continue;
+        T *out = static_cast<T *>(g.out.ptr) + b * g.out.stride_b + n * g.out.stride_n;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int cl = (lane + i * tpr) * kVec;
+            if (cl < g.L) {
+                const int c = c0 + cl, h = c / g.d, j = c % g.d;
+                float w[kVec];
+                load_param<kAligned>(g.w, c, g.L - cl, 1.0f, w);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) v[i][e] = v[i][e] * rs * w[e];
+                store_heads<kAligned>(out, g.out.stride_h, h, j, g.d, g.L - cl, v[i]);
+            }
+        }
+        if (g.rstd && lane == 0) g.rstd[m * g.groups + group] = rs;
+    }
+}
+
+template <typename T, bool kAligned, int kNv, int kMax>
+__global__ void __launch_bounds__(kMax) gated_norm_bwd_kernel(const GatedNormArgs g) {
+    constexpr int kVec = kVecOf<T>;
+    extern __shared__ float sh[];
+    __shared__ float red[2][32];
+    const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr / g.gpb;
+    const int group = blockIdx.y * g.gpb + slot % g.gpb, c0 = group * g.L;
+    const long long tokens = (long long)g.B * g.N;
+    float dw[kNv][kVec] = {};
+    int turn = 0;
+    for (long long m0 = (long long)blockIdx.x * slots; m0 < tokens; m0 += (long long)gridDim.x * slots, ++turn) {
+        const long long m = m0 + slot / g.gpb;
+        const bool on = m < tokens;
+        const long long b = on ? m / g.N : 0, n = on ? m % g.N : 0;
+        const T *x = static_cast<const T *>(g.x.ptr) + b * g.x.stride_b + n * g.x.stride_n;
+        const T *z = g.z.ptr ? static_cast<const T *>(g.z.ptr) + b * g.z.stride_b + n * g.z.stride_n : nullptr;
+        const T *dy = static_cast<const T *>(g.dy.ptr) + b * g.dy.stride_b + n * g.dy.stride_n;
+        const float rs = on ? g.rstd[m * g.groups + group] : 0.0f;
+        float xv[kNv][kVec], gy[kNv][kVec], zv[kNv][kVec], dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int cl = (lane + i * tpr) * kVec;
+            if (on && cl < g.L) {
+                const int c = c0 + cl, h = c / g.d, j = c % g.d;
+                load_heads<kAligned>(x, g.x.stride_h, h, j, g.d, g.L - cl, xv[i]);
+                load_heads<kAligned>(dy, g.dy.stride_h, h, j, g.d, g.L - cl, gy[i]);
+                float w[kVec];
+                load_param<kAligned>(g.w, c, g.L - cl, 1.0f, w);
+                if (z) load_heads<kAligned>(z, g.z.stride_h, h, j, g.d, g.L - cl, zv[i]);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float s = z ? __fdividef(zv[i][e], 1.0f + expf(-zv[i][e])) : 1.0f;
+                    // xhat (.) g is the same product in both orders of gate and norm
+                    const float t = gy[i][e] * s * (xv[i][e] * rs);
+                    dw[i][e] += t;
+                    gy[i][e] *= w[e];
+                    dot = fmaf(t, w[e], dot);
+                }
+            }
+        }
+        dot = row_sum(dot, tpr, red, turn) / g.L;
+        if (!on) continue;
+        T *dx = static_cast<T *>(g.dx.ptr) + b * g.dx.stride_b + n * g.dx.stride_n;
+        T *dz = z ? static_cast<T *>(g.dz.ptr) + b * g.dz.stride_b + n * g.dz.stride_n : nullptr;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int cl = (lane + i * tpr) * kVec;
+            if (cl < g.L) {
+                const int c = c0 + cl, h = c / g.d, j = c % g.d;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    float sig = 0.0f, s = 1.0f;
+                    if (z) {
+                        sig = __fdividef(1.0f, 1.0f + expf(-zv[i][e]));
+                        s = zv[i][e] * sig;
+                    }
+                    const float xx = xv[i][e], gw = gy[i][e];
+                    float ds;
+                    if (g.after) {
+                        xv[i][e] = rs * fmaf(-xx * rs, dot, gw * s);
+                        ds = gw * (xx * rs);
+                    } else {
+                        const float du = rs * fmaf(-xx * s * rs, dot, gw);
+                        xv[i][e] = du * s;
+                        ds = du * xx;
+                    }
+                    if (z) zv[i][e] = ds * sig * fmaf(zv[i][e], 1.0f - sig, 1.0f);
+                }
+                store_heads<kAligned>(dx, g.dx.stride_h, h, j, g.d, g.L - cl, xv[i]);
+                if (z) store_heads<kAligned>(dz, g.dz.stride_h, h, j, g.d, g.L - cl, zv[i]);
+            }
+        }
+    }
+    if (g.part)
+        write_part<kNv, kVec>(dw, sh, slot, slots * g.gpb, lane, tpr, g.gpb, g.L,
+                              g.part + (long long)blockIdx.x * g.H * g.d + c0);
+}
+
+// ------------------------------------------------------------------- wide rows
+// Rows that no block holds in registers: a block walks a row twice, and its
+// partial sums of the parameter gradients are in memory (one thread a channel).
 // Sum over the block, the same in every thread.
 __device__ __forceinline__ float block_sum(float v) {
     __shared__ float red[kThreads / 32];
@@ -40,21 +504,9 @@ __device__ __forceinline__ float block_sum(float v) {
     return s;
 }
 
-struct AddNormArgs {
-    ssd_rows x, res, r, out, dy, dres, dr, dx;
-    const float *scale, *w;
-    float *rstd, *part;
-    int M, C;
-    float eps;
-};
-
-template <typename T>
-__device__ __forceinline__ T *row_of(const ssd_rows &v, long long m) {
-    return v.ptr ? static_cast<T *>(v.ptr) + m * v.stride : nullptr;
-}
 
 template <typename T, typename R>
-__global__ void __launch_bounds__(kThreads) add_norm_kernel(AddNormArgs g) {
+__global__ void __launch_bounds__(kThreads) add_norm_wide_kernel(AddNormArgs g) {
     for (long long m = blockIdx.x; m < g.M; m += gridDim.x) {
         const T *x = row_of<const T>(g.x, m);
         const R *res = row_of<const R>(g.res, m);
@@ -83,7 +535,7 @@ __global__ void __launch_bounds__(kThreads) add_norm_kernel(AddNormArgs g) {
 }
 
 template <typename T, typename R>
-__global__ void __launch_bounds__(kThreads) add_norm_bwd_kernel(AddNormArgs g) {
+__global__ void __launch_bounds__(kThreads) add_norm_bwd_wide_kernel(AddNormArgs g) {
     float *pw = g.part ? g.part + (long long)blockIdx.x * 2 * g.C : nullptr, *ps = pw ? pw + g.C : nullptr;
     if (pw)
         for (int c = threadIdx.x; c < g.C; c += kThreads) pw[c] = ps[c] = 0.0f;
@@ -113,30 +565,12 @@ __global__ void __launch_bounds__(kThreads) add_norm_bwd_kernel(AddNormArgs g) {
     }
 }
 
-// Sums of the slabs' partial rows, in order.
-__global__ void __launch_bounds__(kThreads) sum_parts_kernel(const float *part, int slabs, long long stride, int C,
-                                                            float *out) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= C) return;
-    float s = 0.0f;
-    for (int i = 0; i < slabs; ++i) s += part[i * stride + c];
-    out[c] = s;
-}
-
-struct GatedNormArgs {
-    ssd_view x, z, out, dy, dx, dz;
-    const float *w;
-    float *rstd, *part;
-    int B, H, N, d, groups, after;
-    float eps;
-};
-
 __device__ __forceinline__ long long offset_of(const ssd_view &v, int b, int n, int c, int d) {
     return b * v.stride_b + n * v.stride_n + (c / d) * v.stride_h + c % d;
 }
 
 template <typename T, bool kBackward>
-__global__ void __launch_bounds__(kThreads) gated_norm_kernel(GatedNormArgs g) {
+__global__ void __launch_bounds__(kThreads) gated_norm_wide_kernel(GatedNormArgs g) {
     const int C = g.H * g.d, L = C / g.groups;
     const long long tokens = (long long)g.B * g.N;
     const int c0 = blockIdx.y * L;
@@ -201,7 +635,130 @@ __global__ void __launch_bounds__(kThreads) gated_norm_kernel(GatedNormArgs g) {
     }
 }
 
-unsigned slabs_for(long long rows) { return (unsigned)(rows < 592 ? rows : 592); }
+
+// ------------------------------------------------------------------ the launch
+// How rows of L channels are given to threads: vectors of 16 bytes, `nv` of them
+// a thread, `tpr` threads a row, gpb groups a block side by side; nv = 0: a wide
+// row.  Forward a thread holds up to 32 values of a row, backward 16 (and
+// as many sums).
+struct Cut {
+    int nv, tpr, threads, gpb;
+    unsigned blocks;
+};
+
+constexpr int kSMs = 148;
+constexpr unsigned kMaxParts = 4 * kSMs;  // blocks of a backward pass: bounds its workspace
+
+Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward) {
+    Cut c{};
+    const int vec = (int)(16 / esize), n = (L + vec - 1) / vec, most = backward ? 512 : 1024;
+    c.nv = n <= 32 ? 1 : esize == 4 || !backward ? 4 : 2;
+    c.tpr = 1;
+    while (c.tpr * c.nv < n) c.tpr *= 2;
+    c.gpb = 1;
+    c.threads = kThreads;
+    if (c.tpr > most) {
+        c.nv = 0;
+        c.blocks = (unsigned)(rows < 2 * kSMs ? rows : 2 * kSMs);
+        return c;
+    }
+    if (c.tpr > c.threads) c.threads = c.tpr;
+    // few rows: smaller blocks reach more SMs
+    while (c.threads > 32 && c.threads > c.tpr && rows * groups * c.tpr < (long long)c.threads * kSMs) c.threads /= 2;
+    while (c.gpb * 2 * c.tpr <= c.threads && groups % (c.gpb * 2) == 0) c.gpb *= 2;
+    const long long slots = c.threads / c.tpr / c.gpb, want = (rows + slots - 1) / slots;
+    long long most_blocks = backward ? 2 * kSMs * kThreads / c.threads : 8 * kSMs * kThreads / c.threads;
+    if (backward && most_blocks > kMaxParts) most_blocks = kMaxParts;
+    const unsigned gy = (unsigned)(groups / c.gpb);
+    most_blocks = (most_blocks + gy - 1) / gy;
+    c.blocks = (unsigned)(want < most_blocks ? want : most_blocks);
+    return c;
+}
+
+// Dispatch on alignment, vectors a thread and the largest block.
+#define SSD_NORM_DISPATCH(NVBIG, BIG, RUN)                             \
+    do {                                                               \
+        if (c.nv == 1) {                                               \
+            if (aligned) RUN(true, 1, kThreads);                       \
+            else RUN(false, 1, kThreads);                              \
+        } else if (c.threads <= kThreads) {                            \
+            if (aligned) RUN(true, NVBIG, kThreads);                   \
+            else RUN(false, NVBIG, kThreads);                          \
+        } else {                                                       \
+            if (aligned) RUN(true, NVBIG, BIG);                        \
+            else RUN(false, NVBIG, BIG);                               \
+        }                                                              \
+    } while (0)
+
+template <typename T, typename R>
+void run_add(const AddNormArgs &g, const Cut &c, bool aligned, cudaStream_t s) {
+    if (c.nv == 0) {
+        add_norm_wide_kernel<T, R><<<c.blocks, kThreads, 0, s>>>(g);
+        return;
+    }
+#define RUN(AL, NV, MX) add_norm_kernel<T, R, AL, NV, MX><<<c.blocks, c.threads, 0, s>>>(g)
+    SSD_NORM_DISPATCH(4, 1024, RUN);
+#undef RUN
+}
+
+template <typename T, typename R>
+void run_add_bwd(const AddNormArgs &g, const Cut &c, bool aligned, cudaStream_t s) {
+    if (c.nv == 0) {
+        add_norm_bwd_wide_kernel<T, R><<<c.blocks, kThreads, 0, s>>>(g);
+        return;
+    }
+    const size_t sm = g.part ? (size_t)c.threads * c.nv * kVecOf<T> * sizeof(float) : 0;
+#define RUN(AL, NV, MX) add_norm_bwd_kernel<T, R, AL, NV, MX><<<c.blocks, c.threads, sm, s>>>(g)
+    SSD_NORM_DISPATCH((sizeof(T) == 4 ? 4 : 2), 512, RUN);
+#undef RUN
+}
+
+template <typename T>
+void run_gated(const GatedNormArgs &g, const Cut &c, bool aligned, cudaStream_t s) {
+    if (c.nv == 0) {
+        gated_norm_wide_kernel<T, false><<<dim3(c.blocks, g.groups), kThreads, 0, s>>>(g);
+        return;
+    }
+    const dim3 grid(c.blocks, g.groups / c.gpb);
+#define RUN(AL, NV, MX) gated_norm_kernel<T, AL, NV, MX><<<grid, c.threads, 0, s>>>(g)
+    SSD_NORM_DISPATCH(4, 1024, RUN);
+#undef RUN
+}
+
+template <typename T>
+void run_gated_bwd(const GatedNormArgs &g, const Cut &c, bool aligned, cudaStream_t s) {
+    if (c.nv == 0) {
+        gated_norm_wide_kernel<T, true><<<dim3(c.blocks, g.groups), kThreads, 0, s>>>(g);
+        return;
+    }
+    const dim3 grid(c.blocks, g.groups / c.gpb);
+    const size_t sm = g.part ? (size_t)c.threads * c.nv * kVecOf<T> * sizeof(float) : 0;
+#define RUN(AL, NV, MX) gated_norm_bwd_kernel<T, AL, NV, MX><<<grid, c.threads, sm, s>>>(g)
+    SSD_NORM_DISPATCH((sizeof(T) == 4 ? 4 : 2), 512, RUN);
+#undef RUN
+}
+
+// The second step of the parameter gradients; starts while the first drains.
+int sum_parts(const float *part, unsigned rows, long long stride, int C, float *out0, float *out1, cudaStream_t s) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)((C + 31) / 32), out1 ? 2 : 1);
+    c.blockDim = dim3(256);
+    c.stream = s;
+    c.attrs = pdl;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, sum_parts_kernel, part, (int)rows, stride, C, out0, out1) == cudaSuccess
+               ? SSD_OK : SSD_ERR_CUDA;
+}
+
+bool rows16(const ssd_rows &v, size_t esize) {
+    return !misaligned(v.ptr, 16) && v.stride * (long long)esize % 16 == 0;
+}
+bool view16(const ssd_view &v, size_t esize) {
+    return !misaligned(v.ptr, 16) && ((v.stride_b | v.stride_h | v.stride_n) * (long long)esize) % 16 == 0;
+}
 
 bool eps_ok(float eps) { return eps > 0.0f && eps < 1e30f; }
 
@@ -244,19 +801,23 @@ int ssd_add_norm(const ssd_rows *x, const ssd_rows *residual, const float *scale
     if (r) g.r = *r;
     g.out = *out;
     g.scale = scale, g.w = w, g.rstd = rstd, g.M = M, g.C = C, g.eps = p->eps;
+    const bool aligned = rows16(g.x, e) && rows16(g.out, e) && rows16(g.res, er) && rows16(g.r, er) &&
+                         !misaligned(scale, 16) && !misaligned(w, 16) && (C * e) % 16 == 0;
+    const Cut c = cut_rows(C, M, 1, e, false);
+    g.tpr = c.tpr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == SSD_F32)
-        add_norm_kernel<float, float><<<slabs_for(M), kThreads, 0, s>>>(g);
+        run_add<float, float>(g, c, aligned, s);
     else if (res_dtype == SSD_F32)
-        add_norm_kernel<__nv_bfloat16, float><<<slabs_for(M), kThreads, 0, s>>>(g);
+        run_add<__nv_bfloat16, float>(g, c, aligned, s);
     else
-        add_norm_kernel<__nv_bfloat16, __nv_bfloat16><<<slabs_for(M), kThreads, 0, s>>>(g);
+        run_add<__nv_bfloat16, __nv_bfloat16>(g, c, aligned, s);
     return launched();
 }
 
 size_t ssd_add_norm_bwd_workspace_bytes(int M, int C) {
     if (!sizes_ok(1, 1, M, C)) return 0;
-    return align_up((size_t)slabs_for(M) * 2 * C * sizeof(float), 256);
+    return align_up((size_t)(M < (int)kMaxParts ? M : kMaxParts) * 2 * C * sizeof(float), 256);
 }
 
 int ssd_add_norm_bwd(const ssd_rows *dy, const ssd_rows *r, const float *rstd, const float *w,
@@ -286,17 +847,20 @@ int ssd_add_norm_bwd(const ssd_rows *dy, const ssd_rows *r, const float *rstd, c
     g.scale = scale, g.w = w, g.rstd = const_cast<float *>(rstd), g.M = M, g.C = C;
     if (dw || dscale) g.part = static_cast<float *>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned slabs = slabs_for(M);
+    g.want_scale = dscale != nullptr;
+    const bool aligned = rows16(g.dy, e) && rows16(g.r, er) && rows16(g.dr, er) && rows16(g.x, e) && rows16(g.dres, er) &&
+                         rows16(g.dx, e) && !misaligned(scale, 16) && !misaligned(w, 16) && (C * e) % 16 == 0;
+    const Cut c = cut_rows(C, M, 1, e, true);
+    g.tpr = c.tpr;
     if (dtype == SSD_F32)
-        add_norm_bwd_kernel<float, float><<<slabs, kThreads, 0, s>>>(g);
+        run_add_bwd<float, float>(g, c, aligned, s);
     else if (res_dtype == SSD_F32)
-        add_norm_bwd_kernel<__nv_bfloat16, float><<<slabs, kThreads, 0, s>>>(g);
+        run_add_bwd<__nv_bfloat16, float>(g, c, aligned, s);
     else
-        add_norm_bwd_kernel<__nv_bfloat16, __nv_bfloat16><<<slabs, kThreads, 0, s>>>(g);
-    const unsigned cb = (unsigned)((C + kThreads - 1) / kThreads);
-    if (dw) sum_parts_kernel<<<cb, kThreads, 0, s>>>(g.part, (int)slabs, 2ll * C, C, dw);
-    if (dscale) sum_parts_kernel<<<cb, kThreads, 0, s>>>(g.part + C, (int)slabs, 2ll * C, C, dscale);
-    return launched();
+        run_add_bwd<__nv_bfloat16, __nv_bfloat16>(g, c, aligned, s);
+    rc = launched();
+    if (rc != SSD_OK || !g.part) return rc;
+    return sum_parts(g.part, c.blocks, 2ll * C, C, dw, dscale, s);
 }
 
 int ssd_gated_norm(const ssd_view *x, const ssd_view *z, const float *w, int B, int H, int N, int d_h,
@@ -317,18 +881,24 @@ int ssd_gated_norm(const ssd_view *x, const ssd_view *z, const float *w, int B, 
     g.out = *out;
     g.w = w, g.rstd = rstd, g.B = B, g.H = H, g.N = N, g.d = d_h, g.groups = p->groups;
     g.after = p->flags & SSD_NORM_GATE_AFTER, g.eps = p->eps;
-    const dim3 grid(slabs_for((long long)B * N), p->groups);
+    g.L = H * d_h / p->groups;
+    // a vector lies in one head and one group
+    const bool aligned = view16(g.x, e) && view16(g.z, e) && view16(g.out, e) && !misaligned(w, 16) &&
+                         (d_h * e) % 16 == 0 && (g.L * e) % 16 == 0;
+    const Cut c = cut_rows(g.L, (long long)B * N, g.groups, e, false);
+    g.tpr = c.tpr, g.gpb = c.gpb;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == SSD_F32)
-        gated_norm_kernel<float, false><<<grid, kThreads, 0, s>>>(g);
+        run_gated<float>(g, c, aligned, s);
     else
-        gated_norm_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(g);
+        run_gated<__nv_bfloat16>(g, c, aligned, s);
     return launched();
 }
 
 size_t ssd_gated_norm_bwd_workspace_bytes(int B, int H, int N, int d_h, int groups) {
     if (check_gated(B, H, N, d_h, SSD_F32, groups) != SSD_OK) return 0;
-    return align_up((size_t)slabs_for((long long)B * N) * H * d_h * sizeof(float), 256);
+    const long long rows = (long long)B * N;
+    return align_up((size_t)(rows < kMaxParts ? rows : kMaxParts) * H * d_h * sizeof(float), 256);
 }
 
 int ssd_gated_norm_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *z, const float *w,
@@ -357,16 +927,19 @@ int ssd_gated_norm_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *z,
     g.w = w, g.rstd = const_cast<float *>(rstd), g.B = B, g.H = H, g.N = N, g.d = d_h, g.groups = p->groups;
     g.after = p->flags & SSD_NORM_GATE_AFTER;
     if (dw) g.part = static_cast<float *>(workspace);
-    const unsigned slabs = slabs_for((long long)B * N);
-    const dim3 grid(slabs, p->groups);
+    g.L = H * d_h / p->groups;
+    const bool aligned = view16(g.dy, e) && view16(g.x, e) && view16(g.z, e) && view16(g.dx, e) && view16(g.dz, e) &&
+                         !misaligned(w, 16) && (d_h * e) % 16 == 0 && (g.L * e) % 16 == 0;
+    const Cut c = cut_rows(g.L, (long long)B * N, g.groups, e, true);
+    g.tpr = c.tpr, g.gpb = c.gpb;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == SSD_F32)
-        gated_norm_kernel<float, true><<<grid, kThreads, 0, s>>>(g);
+        run_gated_bwd<float>(g, c, aligned, s);
     else
-        gated_norm_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(g);
-    const int C = H * d_h;
-    if (dw) sum_parts_kernel<<<(C + kThreads - 1) / kThreads, kThreads, 0, s>>>(g.part, (int)slabs, C, C, dw);
-    return launched();
+        run_gated_bwd<__nv_bfloat16>(g, c, aligned, s);
+    rc = launched();
+    if (rc != SSD_OK || !dw) return rc;
+    return sum_parts(g.part, c.blocks, (long long)H * d_h, H * d_h, dw, nullptr, s);
 }
 
 }  // extern "C"

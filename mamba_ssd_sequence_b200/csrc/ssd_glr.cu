@@ -37,15 +37,17 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(const Args g, int mo
     const float gv = to_f32(static_cast<const T *>(g.gate.ptr)[b * g.gate.stride_b + h * g.gate.stride_h + j]);
     const float h0 = g.h0[i];
     const float rate = g.A_log ? expf(g.A_log[c]) : 1.0f, bias = g.dt_bias ? g.dt_bias[c] : 0.0f;
-    float a, f;
+    // (both halves of the pairwise forms take the channel)
+    const float2 g2 = both(gv), b2 = both(bias), r2 = both(rate);
+    float2 a, f;
     switch (mode) {
-    case kDtNone: a = gate_of<kDtNone>(gv, bias, rate, &f); break;
-    case kDtDt: a = gate_of<kDtDt>(gv, bias, rate, &f); break;
-    case kDtComplement: a = gate_of<kDtComplement>(gv, bias, rate, &f); break;
-    case kLogNone: a = gate_of<kLogNone>(gv, bias, rate, &f); break;
-    default: a = gate_of<kLogComplement>(gv, bias, rate, &f); break;
+    case kDtNone: a = gate_of<kDtNone>(g2, b2, r2, &f); break;
+    case kDtDt: a = gate_of<kDtDt>(g2, b2, r2, &f); break;
+    case kDtComplement: a = gate_of<kDtComplement>(g2, b2, r2, &f); break;
+    case kLogNone: a = gate_of<kLogNone>(g2, b2, r2, &f); break;
+    default: a = gate_of<kLogComplement>(g2, b2, r2, &f); break;
     }
-    const float y = fmaf(a, h0, f * xv);
+    const float y = fmaf(a.x, h0, f.x * xv);
     g.h_out[i] = y;
     store_one(static_cast<T *>(g.out.ptr) + b * g.out.stride_b + h * g.out.stride_h + j, y);
 }

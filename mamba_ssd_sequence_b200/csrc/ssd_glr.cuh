@@ -58,6 +58,34 @@ struct Tile {
     static constexpr int bytes = segs * seg;          // one activation
 };
 
+// Two channels at once: sm_100a issues two fp32 operations as one.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
 __device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 __device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
     const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
@@ -75,54 +103,61 @@ __device__ __forceinline__ float minus_infinity() { return __uint_as_float(0xFF8
 
 // q(t) of 1 - exp(-t) = t q(t) for |t| < 1/2 (coefficients from
 // mamba_ssd_sequence_b200/gen_decay_poly.py, relative error 2.1e-7).
-__device__ __forceinline__ float decay_poly(float t) {
-    float p = -1.398218563e-03f;
-    p = fmaf(p, t, 8.408029564e-03f);
-    p = fmaf(p, t, -4.166579247e-02f);
-    p = fmaf(p, t, 1.666596532e-01f);
-    p = fmaf(p, t, -5.000000000e-01f);
-    return fmaf(p, t, 1.000000119e+00f);
+__device__ __forceinline__ float2 decay_poly(float2 t) {
+    float2 p = both(-1.398218563e-03f);
+    p = fma2(p, t, both(8.408029564e-03f));
+    p = fma2(p, t, both(-4.166579247e-02f));
+    p = fma2(p, t, both(1.666596532e-01f));
+    p = fma2(p, t, both(-5.000000000e-01f));
+    return fma2(p, t, both(1.000000119e+00f));
 }
 
 // a = exp(-t) and 1 - a.  Near t = 0 the hardware exponential's error (2^-22)
 // would have one sign over the many tokens that a slow decay spans, and add
 // up; 1 - t q(t) is rounded once, either way, and its 1 - a is exact to its
 // last bits.
-__device__ __forceinline__ float decay_of(float t, float *one_minus) {
-    const float w = t * decay_poly(t), e = ptx::ex2_approx(t * -1.4426950408889634f);
-    const bool small = fabsf(t) < 0.5f;
-    *one_minus = small ? w : 1.0f - e;
-    return small ? 1.0f - w : e;
+__device__ __forceinline__ float2 decay_of(float2 t, float2 *one_minus) {
+    const float2 q = decay_poly(t), w = mul2(t, q), c = fma2(neg2(t), q, both(1.0f));
+    const float2 e = make_float2(ptx::ex2_approx(t.x * -1.4426950408889634f), ptx::ex2_approx(t.y * -1.4426950408889634f));
+    const bool sx = fabsf(t.x) < 0.5f, sy = fabsf(t.y) < 0.5f;
+    *one_minus = make_float2(sx ? w.x : 1.0f - e.x, sy ? w.y : 1.0f - e.y);
+    return make_float2(sx ? c.x : e.x, sy ? c.y : e.y);
 }
 
-// dt = softplus(p) (softplus_fast of ssd_math.cuh) and d dt / d p = sigmoid(p).
-__device__ __forceinline__ float softplus_slope(float p, float *slope) {
-    const float u = ptx::ex2_approx(-fabsf(p) * 1.4426950408889634f);
-    float q = 5.126102362e-03f;
-    q = fmaf(q, u, -2.907406539e-02f);
-    q = fmaf(q, u, 7.751608640e-02f);
-    q = fmaf(q, u, -1.360224783e-01f);
-    q = fmaf(q, u, 1.907688081e-01f);
-    q = fmaf(q, u, -2.483539879e-01f);
-    q = fmaf(q, u, 3.331812024e-01f);
-    q = fmaf(q, u, -4.999944568e-01f);
-    q = fmaf(q, u, 9.999999404e-01f);
-    *slope = __fdividef(p >= 0.0f ? 1.0f : u, 1.0f + u);
-    return fmaxf(p, 0.0f) + u * q;
+// dt = softplus(p) = max(p, 0) + log1p(exp(-|p|)), the polynomial of
+// softplus_fast (ssd_math.cuh); u receives exp(-|p|).
+__device__ __forceinline__ float2 softplus2(float2 p, float2 *u_out) {
+    const float2 u = make_float2(ptx::ex2_approx(-fabsf(p.x) * 1.4426950408889634f),
+                                 ptx::ex2_approx(-fabsf(p.y) * 1.4426950408889634f));
+    float2 q = both(5.126102362e-03f);
+    q = fma2(q, u, both(-2.907406539e-02f));
+    q = fma2(q, u, both(7.751608640e-02f));
+    q = fma2(q, u, both(-1.360224783e-01f));
+    q = fma2(q, u, both(1.907688081e-01f));
+    q = fma2(q, u, both(-2.483539879e-01f));
+    q = fma2(q, u, both(3.331812024e-01f));
+    q = fma2(q, u, both(-4.999944568e-01f));
+    q = fma2(q, u, both(9.999999404e-01f));
+    *u_out = u;
+    return fma2(u, q, make_float2(fmaxf(p.x, 0.0f), fmaxf(p.y, 0.0f)));
+}
+// d dt / d p = sigmoid(p), from u = exp(-|p|)
+__device__ __forceinline__ float slope_of(float p, float u) {
+    return __fdividef(p >= 0.0f ? 1.0f : u, 1.0f + u);
 }
 
-// One token of one channel: the decay a, the factor f of x.
+// One token of two channels: the decay a, the factor f of x.
 template <int kMode>
-__device__ __forceinline__ float gate_of(float g, float bias, float rate, float *f) {
-    float w, s = 0.0f, t;
+__device__ __forceinline__ float2 gate_of(float2 g, float2 bias, float2 rate, float2 *f) {
+    float2 w, s = both(0.0f), t, u;
     if (ModeOf<kMode>::log) {
-        t = -g;
+        t = neg2(g);
     } else {
-        s = softplus_fast(g + bias);
-        t = rate * s;
+        s = softplus2(add2(g, bias), &u);
+        t = mul2(rate, s);
     }
-    const float a = decay_of(t, &w);
-    *f = ModeOf<kMode>::dt ? s : ModeOf<kMode>::complement ? w : 1.0f;
+    const float2 a = decay_of(t, &w);
+    *f = ModeOf<kMode>::dt ? s : ModeOf<kMode>::complement ? w : both(1.0f);
     return a;
 }
 
@@ -155,18 +190,23 @@ __device__ __forceinline__ void fetch_tile(unsigned char *dst, const T *base, lo
                                            int c0, int d, bool aligned) {
     using Tl = Tile<T, kCb>;
     if (aligned) {
-        constexpr int vec = 16 / sizeof(T), cpr = kCb / vec, per_thread = Tl::tok * cpr / Tl::nt;
-        const int col = (threadIdx.x % cpr) * vec;
-        const int row0 = threadIdx.x / cpr;
+        constexpr int vec = 16 / sizeof(T), cpr = kCb / vec, per_thread = Tl::tok * cpr / Tl::nt, step = Tl::nt / cpr;
+        constexpr int pad = Tl::seg - kSeg * Tl::row;
+        static_assert(step % kSeg == 0 || pad == 0, "the thread's rows are evenly spaced in shared memory");
+        const int col = (threadIdx.x % cpr) * vec, row0 = threadIdx.x / cpr;
         const bool cv = c0 + col < d;
-        const uint32_t s0 = ptx::smem_u32(dst) + col * (int)sizeof(T);
+        uint32_t s = ptx::smem_u32(dst) + col * (int)sizeof(T) + row0 * Tl::row + row0 / kSeg * pad;
+        const T *p = cv ? base + (t0 + row0) * stride_n + c0 + col : base;
+        const long long hop = cv ? step * stride_n : 0;
+        if (t0 + Tl::tok <= len) {
 #pragma unroll
-        for (int i = 0; i < per_thread; ++i) {
-            const int row = row0 + i * (Tl::nt / cpr);
-            const long long t = t0 + row;
-            const bool v = cv && t < len;
-            cp_async16(s0 + (row / kSeg) * Tl::seg + (row % kSeg) * Tl::row,
-                       v ? static_cast<const void *>(base + t * stride_n + c0 + col) : base, v);
+            for (int i = 0; i < per_thread; ++i, p += hop) cp_async16(s + i * (step * Tl::row + step / kSeg * pad), p, cv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < per_thread; ++i, p += hop) {
+                const bool v = cv && t0 + row0 + i * step < len;
+                cp_async16(s + i * (step * Tl::row + step / kSeg * pad), v ? p : base, v);
+            }
         }
     } else {
         for (int e = threadIdx.x; e < Tl::tok * kCb; e += Tl::nt) {
@@ -242,16 +282,14 @@ __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, float
     }
     if (in_warp == (kForward ? Tl::per_warp - 1 : 0)) warp_maps[warp * Tl::lanes + lane] = upto;
     __syncthreads();
-    float4 base = identity_map();
-#pragma unroll
-    for (int i = 0; i < Tl::warps; ++i) {
-        const int w = kForward ? i : Tl::warps - 1 - i;
-        if (kForward ? w < warp : w > warp) base = then(base, warp_maps[w * Tl::lanes + lane]);
-    }
+    // the first threads behind the tile's last segment join the tile's map
     tile_maps += (round & 1) * 8 * Tl::lanes;
-    const bool last = kForward ? (warp == Tl::warps - 1 && in_warp == Tl::per_warp - 1) : (warp == 0 && in_warp == 0);
-    if (last) {
-        const float4 all = then(base, upto);
+    const int last_warp = kForward ? Tl::warps - 1 : 0;
+    if (warp == last_warp && in_warp == (kForward ? Tl::per_warp - 1 : 0)) {
+        float4 all = warp_maps[(kForward ? 0 : Tl::warps - 1) * Tl::lanes + lane];
+#pragma unroll
+        for (int i = 1; i < Tl::warps - 1; ++i) all = then(all, warp_maps[(kForward ? i : Tl::warps - 1 - i) * Tl::lanes + lane]);
+        all = then(all, upto);
         float4 *slot = tile_maps + rank * Tl::lanes + lane;
         if (cluster == 1) {
             *slot = all;
@@ -272,7 +310,12 @@ __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, float
         if (r == rank) h = carry;
         carry = apply(tile_maps[r * Tl::lanes + lane], carry);
     }
-    return apply(before, apply(base, h));
+    if (kForward) {
+        for (int w = 0; w < warp; ++w) h = apply(warp_maps[w * Tl::lanes + lane], h);
+    } else {
+        for (int w = Tl::warps - 1; w > warp; --w) h = apply(warp_maps[w * Tl::lanes + lane], h);
+    }
+    return Tl::per_warp > 1 ? apply(before, h) : h;
 }
 
 // How a call is cut up: blocks of cb channels, and `cluster` blocks that share

@@ -111,55 +111,75 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
         next_state = state_at(i + 1);
         // a, and q = a h_{t-1} (a (h_{t-1} - x) for f = 1 - a): d log a = l q
         float2 a[kSeg], q[kSeg];
-        float4 own = identity_map();  // l entering the segment -> a_0 l_0
+        float2 prod = both(1.0f), first = both(0.0f);  // l behind the segment -> a_0 l_0
 #pragma unroll
         for (int k = 0; k < kSeg; ++k) {
             const float2 xv = load_pair(xc + k * kCb), gv = load_pair(gc + k * kCb), yv = load_pair(yc + k * kCb);
             float2 f;
-            a[k].x = gate_of<kMode>(gv.x, bias.x, rate.x, &f.x);
-            a[k].y = gate_of<kMode>(gv.y, bias.y, rate.y, &f.y);
-            const float2 ah = make_float2(a[k].x * hs.x, a[k].y * hs.y);
-            q[k] = M::complement ? make_float2(fmaf(-a[k].x, xv.x, ah.x), fmaf(-a[k].y, xv.y, ah.y)) : ah;
-            hs = make_float2(fmaf(f.x, xv.x, ah.x), fmaf(f.y, xv.y, ah.y));
-            own.x *= a[k].x, own.z *= a[k].y;
-            own.y = fmaf(own.x, yv.x, own.y), own.w = fmaf(own.z, yv.y, own.w);
+            a[k] = gate_of<kMode>(gv, bias, rate, &f);
+            const float2 ah = mul2(a[k], hs);
+            q[k] = M::complement ? fma2(neg2(a[k]), xv, ah) : ah;
+            hs = kMode == kDtNone || kMode == kLogNone ? add2(ah, xv) : fma2(f, xv, ah);
+            prod = mul2(prod, a[k]);
+            first = fma2(prod, yv, first);
         }
+        const float4 own = make_float4(prod.x, first.x, prod.y, first.y);
         float2 lc = enter_segment<T, kCb, false>(own, carry, warp_maps, tile_maps, i, rank, (int)cluster);
-        float2 segA = make_float2(0.0f, 0.0f), segb = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int k = kSeg - 1; k >= 0; --k) {
-            const float2 yv = load_pair(yc + k * kCb), gv = load_pair(gc + k * kCb), xv = load_pair(xc + k * kCb);
-            float2 vx, vg;
-            auto channel = [&](float y, float gt, float xx, float av, float qv, float bs, float rt, float &lcar, float &sA,
-                               float &sb, float &ox, float &og) {
-                const float l = lcar + y;
-                lcar = av * l;
-                const float dla = l * qv;
-                float f = 1.0f;
-                if (M::log) {
-                    og = dla;
-                    if (M::complement) (void)decay_of(-gt, &f);
-                } else {
-                    float slope;
-                    const float s = softplus_slope(gt + bs, &slope), t = rt * s;
-                    if (M::complement) f = fabsf(t) < 0.5f ? t * decay_poly(t) : 1.0f - av;
-                    if (M::dt) f = s;
-                    float ds = -rt * dla;
-                    if (M::dt) ds = fmaf(l, xx, ds);
-                    og = ds * slope;
-                    // where a = 0 log a may be -infinity, and the product is 0
-                    sA = fmaf(dla, fmaxf(-t, -200.0f), sA);
-                    sb += og;
+        float2 segA = both(0.0f), segb = both(0.0f);
+        // token k: the gradients of x and the gate
+        auto token = [&](int k, float2 *vx, float2 *vg) {
+            const float2 yv = load_pair(yc + k * kCb);
+            const float2 l = add2(lc, yv);
+            lc = mul2(a[k], l);
+            const float2 dla = mul2(l, q[k]);
+            if (M::log) {
+                *vg = dla;
+                *vx = l;
+                if (M::complement) {
+                    float2 w;
+                    (void)decay_of(neg2(load_pair(gc + k * kCb)), &w);
+                    *vx = mul2(w, l);
                 }
-                ox = f * l;
-            };
-            channel(yv.x, gv.x, xv.x, a[k].x, q[k].x, bias.x, rate.x, lc.x, segA.x, segb.x, vx.x, vg.x);
-            channel(yv.y, gv.y, xv.y, a[k].y, q[k].y, bias.y, rate.y, lc.y, segA.y, segb.y, vx.y, vg.y);
-            const long long t = t0 + k;
-            if (k >= valid) vx = vg = make_float2(0.0f, 0.0f);
-            if (t < g.N) {
-                store(dx + t * g.dx.stride_n, vx);
-                store(dgate + t * g.dgate.stride_n, vg);
+                return;
+            }
+            float2 u;
+            const float2 p = add2(load_pair(gc + k * kCb), bias), s = softplus2(p, &u), t = mul2(rate, s);
+            float2 ds = mul2(neg2(rate), dla);
+            *vx = l;
+            if (M::dt) {
+                *vx = mul2(s, l);
+                ds = fma2(l, load_pair(xc + k * kCb), ds);
+            }
+            if (M::complement) {
+                const float2 w = mul2(t, decay_poly(t));
+                *vx = mul2(make_float2(fabsf(t.x) < 0.5f ? w.x : 1.0f - a[k].x, fabsf(t.y) < 0.5f ? w.y : 1.0f - a[k].y), l);
+            }
+            *vg = mul2(ds, make_float2(slope_of(p.x, u.x), slope_of(p.y, u.y)));
+            // where a = 0 log a may be -infinity, and the product is 0
+            segA = fma2(neg2(dla), make_float2(fminf(t.x, 200.0f), fminf(t.y, 200.0f)), segA);
+            segb = add2(segb, *vg);
+        };
+        if (g.aligned && valid == kSeg) {
+            T *ox = dx + (t0 + kSeg - 1) * g.dx.stride_n, *og = dgate + (t0 + kSeg - 1) * g.dgate.stride_n;
+#pragma unroll
+            for (int k = kSeg - 1; k >= 0; --k, ox -= g.dx.stride_n, og -= g.dgate.stride_n) {
+                float2 vx, vg;
+                token(k, &vx, &vg);
+                if (on0) {
+                    store_pair(ox, vx);
+                    store_pair(og, vg);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = kSeg - 1; k >= 0; --k) {
+                float2 vx, vg;
+                token(k, &vx, &vg);
+                if (k >= valid) vx = vg = both(0.0f);
+                if (t0 + k < g.N) {
+                    store(dx + (t0 + k) * g.dx.stride_n, vx);
+                    store(dgate + (t0 + k) * g.dgate.stride_n, vg);
+                }
             }
         }
         sumA = make_float2(sumA.x + segA.x, sumA.y + segA.y);

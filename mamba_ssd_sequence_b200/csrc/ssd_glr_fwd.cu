@@ -95,25 +95,34 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         const int valid = (int)max(0ll, min((long long)kSeg, len - t0));
         if (!M::log && valid < kSeg) close_gates<T, kCb>(gc, valid);
         float2 a[kSeg], u[kSeg];
-        float4 own = identity_map();
+        float2 prod = both(1.0f), end = both(0.0f);
 #pragma unroll
         for (int k = 0; k < kSeg; ++k) {
             const float2 xv = load_pair(xc + k * kCb), gv = load_pair(gc + k * kCb);
             float2 f;
-            a[k].x = gate_of<kMode>(gv.x, bias.x, rate.x, &f.x);
-            a[k].y = gate_of<kMode>(gv.y, bias.y, rate.y, &f.y);
-            u[k] = make_float2(f.x * xv.x, f.y * xv.y);
-            own = then(own, make_float4(a[k].x, u[k].x, a[k].y, u[k].y));
+            a[k] = gate_of<kMode>(gv, bias, rate, &f);
+            u[k] = kMode == kDtNone || kMode == kLogNone ? xv : mul2(f, xv);
+            prod = mul2(prod, a[k]);
+            end = fma2(a[k], end, u[k]);
         }
+        const float4 own = make_float4(prod.x, end.x, prod.y, end.y);
         float2 hs = enter_segment<T, kCb, true>(own, carry, warp_maps, tile_maps, r, rank, (int)cluster);
         if (states && t0 < g.N) save(t0 / kSeg, hs);
+        if (g.aligned && valid == kSeg) {
+            if (on0) {
+                T *o = out + t0 * g.out.stride_n;
 #pragma unroll
-        for (int k = 0; k < kSeg; ++k) {
-            hs = make_float2(fmaf(a[k].x, hs.x, u[k].x), fmaf(a[k].y, hs.y, u[k].y));
-            if (k < valid)
-                store(t0 + k, hs);
-            else if (t0 + k < g.N)
-                store(t0 + k, make_float2(0.0f, 0.0f));
+                for (int k = 0; k < kSeg; ++k, o += g.out.stride_n) {
+                    hs = fma2(a[k], hs, u[k]);
+                    store_pair(o, hs);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSeg; ++k) {
+                hs = fma2(a[k], hs, u[k]);
+                if (t0 + k < g.N) store(t0 + k, k < valid ? hs : both(0.0f));
+            }
         }
     }
     cp_async_wait<0>();

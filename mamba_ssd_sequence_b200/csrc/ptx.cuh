@@ -151,6 +151,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
         if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
+// The same without an abort flag.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+    const int never = 0;
+    return mbar_wait_cluster(bar, parity, &never);
+}
 // Store to the shared memory of CTA `rank` of the cluster (address from mapa_shared).
 __device__ __forceinline__ void st_dsmem_u32(uint32_t cluster_addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");

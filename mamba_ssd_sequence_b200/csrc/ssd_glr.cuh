@@ -173,13 +173,14 @@ template <int n>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
-__device__ __forceinline__ void st_dsmem_f4(uint32_t cluster_addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x), "f"(v.y), "f"(v.z),
-                 "f"(v.w)
+// Writes 16 bytes to a block of the cluster and counts them at its mbarrier:
+// the reader needs no fence, and the writer's other stores are not waited for.
+__device__ __forceinline__ void st_async_f4(uint32_t cluster_addr, uint32_t cluster_bar, float4 v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(
+                     cluster_addr),
+                 "r"(cluster_bar), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Fetches a tile of one activation (base: its token 0, channel 0; tokens from
 // t0, channels from c0) into shared memory.  Places at or behind token `len`
@@ -258,15 +259,45 @@ __device__ __forceinline__ float4 shift(float4 m, int n) {
     return r;
 }
 
+// What the threads of a block, and the blocks of a cluster, tell one another:
+// the maps of the block's warps, and those of the cluster's tiles for two
+// rounds, each with an mbarrier that counts the tiles' bytes.  A block sends
+// round r + 2 after it has every tile of round r + 1, whose block had then read
+// round r: two rounds' places are enough.
+template <int kLanes, int kWarps>
+struct Maps {
+    float4 warp[kWarps][kLanes];
+    float4 tile[2][8][kLanes];
+    uint64_t bar[2];
+};
+template <typename T, int kCb>
+using MapsOf = Maps<Tile<T, kCb>::lanes, Tile<T, kCb>::warps>;
+
+// Before the first round; ends with a barrier of the cluster, since peers may
+// send as soon as they have passed it.
+template <typename M>
+__device__ __forceinline__ void init_maps(M *m, int cluster) {
+    if (cluster == 1) return;
+    if (threadIdx.x == 0) {
+        const uint32_t bytes = (uint32_t)cluster * sizeof(m->tile[0][0]);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&m->bar[i], 1);
+            ptx::mbar_arrive_expect_tx(&m->bar[i], bytes);
+        }
+        ptx::fence_mbar_init();
+    }
+    ptx::cluster_sync_all();
+}
+
 // The state (or, kForward false, the adjoint) that enters this thread's
 // segment, given the segment's own map and the carry that enters the round's
 // first tile (the last one, backwards); the carry is advanced over the whole
-// round.  `warp_maps` is [warps][lanes], `tile_maps` [2][8][lanes] (two
-// rounds' worth: a block may write the next round's while its peers still
-// read this one's).  Every thread of the cluster takes part.
+// round.  Every thread of the cluster takes part.  A wait that runs out (never
+// expected: the blocks of a cluster run together) makes the carry NaN and is
+// not repeated.
 template <typename T, int kCb, bool kForward>
-__device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, float4 *warp_maps, float4 *tile_maps,
-                                                int round, int rank, int cluster) {
+__device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, MapsOf<T, kCb> *maps, int round, int rank,
+                                                int cluster, bool &lost) {
     using Tl = Tile<T, kCb>;
     const int lane = threadIdx.x % Tl::lanes, warp = threadIdx.x / 32, in_warp = (threadIdx.x % 32) / Tl::lanes;
     // the maps of the segments before this one in its warp, and up to it
@@ -280,40 +311,41 @@ __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, float
         const float4 o = shift<kForward>(upto, Tl::lanes);
         if (kForward ? in_warp > 0 : in_warp + 1 < Tl::per_warp) before = o;
     }
-    if (in_warp == (kForward ? Tl::per_warp - 1 : 0)) warp_maps[warp * Tl::lanes + lane] = upto;
+    if (in_warp == (kForward ? Tl::per_warp - 1 : 0)) maps->warp[warp][lane] = upto;
     __syncthreads();
-    // the first threads behind the tile's last segment join the tile's map
-    tile_maps += (round & 1) * 8 * Tl::lanes;
-    const int last_warp = kForward ? Tl::warps - 1 : 0;
-    if (warp == last_warp && in_warp == (kForward ? Tl::per_warp - 1 : 0)) {
-        float4 all = warp_maps[(kForward ? 0 : Tl::warps - 1) * Tl::lanes + lane];
+    // the threads of the tile's last segment join the tile's map
+    const int two = round & 1;
+    if (warp == (kForward ? Tl::warps - 1 : 0) && in_warp == (kForward ? Tl::per_warp - 1 : 0)) {
+        float4 all = maps->warp[kForward ? 0 : Tl::warps - 1][lane];
 #pragma unroll
-        for (int i = 1; i < Tl::warps - 1; ++i) all = then(all, warp_maps[(kForward ? i : Tl::warps - 1 - i) * Tl::lanes + lane]);
+        for (int i = 1; i < Tl::warps - 1; ++i) all = then(all, maps->warp[kForward ? i : Tl::warps - 1 - i][lane]);
         all = then(all, upto);
-        float4 *slot = tile_maps + rank * Tl::lanes + lane;
+        float4 *slot = &maps->tile[two][rank][lane];
         if (cluster == 1) {
             *slot = all;
         } else {
-            const uint32_t at = ptx::smem_u32(slot);
-            for (int r = 0; r < cluster; ++r) st_dsmem_f4(ptx::mapa_shared(at, r), all);
+            const uint32_t at = ptx::smem_u32(slot), bar = ptx::smem_u32(&maps->bar[two]);
+            for (int r = 0; r < cluster; ++r) st_async_f4(ptx::mapa_shared(at, r), ptx::mapa_shared(bar, r), all);
         }
     }
     if (cluster == 1) {
         __syncthreads();
     } else {
-        cluster_arrive();
-        cluster_wait();
+        if (!lost) lost = !ptx::mbar_wait_cluster(&maps->bar[two], (round >> 1) & 1);
+        if (lost) carry = both(__uint_as_float(0x7FC00000u));
+        // every thread waits for this phase itself; the next one's bytes are announced here
+        if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&maps->bar[two], (uint32_t)cluster * sizeof(maps->tile[0][0]));
     }
     float2 h = carry;
     for (int i = 0; i < cluster; ++i) {
         const int r = kForward ? i : cluster - 1 - i;
         if (r == rank) h = carry;
-        carry = apply(tile_maps[r * Tl::lanes + lane], carry);
+        carry = apply(maps->tile[two][r][lane], carry);
     }
     if (kForward) {
-        for (int w = 0; w < warp; ++w) h = apply(warp_maps[w * Tl::lanes + lane], h);
+        for (int w = 0; w < warp; ++w) h = apply(maps->warp[w][lane], h);
     } else {
-        for (int w = Tl::warps - 1; w > warp; --w) h = apply(warp_maps[w * Tl::lanes + lane], h);
+        for (int w = Tl::warps - 1; w > warp; --w) h = apply(maps->warp[w][lane], h);
     }
     return Tl::per_warp > 1 ? apply(before, h) : h;
 }

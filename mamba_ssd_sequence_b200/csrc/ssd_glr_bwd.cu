@@ -24,7 +24,7 @@ constexpr int kStages = 2;
 template <typename T, int kCb>
 constexpr size_t smem_bytes() {
     using Tl = Tile<T, kCb>;
-    return (size_t)kStages * 3 * Tl::bytes + (Tl::warps + 16) * Tl::lanes * sizeof(float4);
+    return (size_t)kStages * 3 * Tl::bytes + sizeof(MapsOf<T, kCb>);
 }
 
 template <typename T, int kCb, int kMode>
@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
     using Tl = Tile<T, kCb>;
     using M = ModeOf<kMode>;
     extern __shared__ __align__(128) unsigned char sm[];
-    float4 *warp_maps = reinterpret_cast<float4 *>(sm + kStages * 3 * Tl::bytes);
-    float4 *tile_maps = warp_maps + Tl::warps * Tl::lanes;
+    auto *maps = reinterpret_cast<MapsOf<T, kCb> *>(sm + kStages * 3 * Tl::bytes);
 
     uint32_t cluster;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
@@ -96,6 +95,8 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
     };
     float2 sumA = make_float2(0.0f, 0.0f), sumb = make_float2(0.0f, 0.0f);
 
+    init_maps(maps, (int)cluster);
+    bool lost = false;
     for (int i = 0; i < rounds; ++i) {
         cp_async_wait<kStages - 2>();
         __syncthreads();  // this round has arrived for every thread, and the one before it is consumed
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
             first = fma2(prod, yv, first);
         }
         const float4 own = make_float4(prod.x, first.x, prod.y, first.y);
-        float2 lc = enter_segment<T, kCb, false>(own, carry, warp_maps, tile_maps, i, rank, (int)cluster);
+        float2 lc = enter_segment<T, kCb, false>(own, carry, maps, i, rank, (int)cluster, lost);
         float2 segA = both(0.0f), segb = both(0.0f);
         // token k: the gradients of x and the gate
         auto token = [&](int k, float2 *vx, float2 *vg) {

@@ -22,7 +22,7 @@ constexpr int kStages = 3;
 template <typename T, int kCb>
 constexpr size_t smem_bytes() {
     using Tl = Tile<T, kCb>;
-    return (size_t)kStages * 2 * Tl::bytes + (Tl::warps + 16) * Tl::lanes * sizeof(float4);
+    return (size_t)kStages * 2 * Tl::bytes + sizeof(MapsOf<T, kCb>);
 }
 
 template <typename T, int kCb, int kMode>
@@ -30,8 +30,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
     using Tl = Tile<T, kCb>;
     using M = ModeOf<kMode>;
     extern __shared__ __align__(128) unsigned char sm[];
-    float4 *warp_maps = reinterpret_cast<float4 *>(sm + kStages * 2 * Tl::bytes);
-    float4 *tile_maps = warp_maps + Tl::warps * Tl::lanes;
+    auto *maps = reinterpret_cast<MapsOf<T, kCb> *>(sm + kStages * 2 * Tl::bytes);
 
     uint32_t cluster;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
@@ -84,6 +83,8 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         if (on1) states[chunk * g.d + 1] = v.y;
     };
 
+    init_maps(maps, (int)cluster);
+    bool lost = false;
     for (int r = 0; r < rounds; ++r) {
         cp_async_wait<kStages - 2>();
         __syncthreads();  // round r has arrived for every thread, and round r - 1 is consumed
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
             end = fma2(a[k], end, u[k]);
         }
         const float4 own = make_float4(prod.x, end.x, prod.y, end.y);
-        float2 hs = enter_segment<T, kCb, true>(own, carry, warp_maps, tile_maps, r, rank, (int)cluster);
+        float2 hs = enter_segment<T, kCb, true>(own, carry, maps, r, rank, (int)cluster, lost);
         if (states && t0 < g.N) save(t0 / kSeg, hs);
         if (g.aligned && valid == kSeg) {
             if (on0) {

@@ -27,6 +27,15 @@ namespace {
 
 constexpr int kThreads = 128;
 
+// One token of one channel (both halves of the pairwise forms take it).
+template <int kMode>
+__device__ __forceinline__ float step(float g, float bias, float nrate2, float x, float h) {
+    const Gate o = gate_of<kMode>(both(g), both(bias), both(nrate2));
+    float2 w;
+    const float a = exact_decay(o.l, &w).x;  // steps follow one another: as exact as a segment's product
+    return fmaf(a, h, value_of<kMode>(o, both(x)).x);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) glr_step_kernel(const Args g, int mode) {
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -36,18 +45,15 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(const Args g, int mo
     const float xv = to_f32(static_cast<const T *>(g.x.ptr)[b * g.x.stride_b + h * g.x.stride_h + j]);
     const float gv = to_f32(static_cast<const T *>(g.gate.ptr)[b * g.gate.stride_b + h * g.gate.stride_h + j]);
     const float h0 = g.h0[i];
-    const float rate = g.A_log ? expf(g.A_log[c]) : 1.0f, bias = g.dt_bias ? g.dt_bias[c] : 0.0f;
-    // (both halves of the pairwise forms take the channel)
-    const float2 g2 = both(gv), b2 = both(bias), r2 = both(rate);
-    float2 a, f;
+    const float nrate2 = -1.4426950408889634f * (g.A_log ? expf(g.A_log[c]) : 1.0f), bias = g.dt_bias ? g.dt_bias[c] : 0.0f;
+    float y;
     switch (mode) {
-    case kDtNone: a = gate_of<kDtNone>(g2, b2, r2, &f); break;
-    case kDtDt: a = gate_of<kDtDt>(g2, b2, r2, &f); break;
-    case kDtComplement: a = gate_of<kDtComplement>(g2, b2, r2, &f); break;
-    case kLogNone: a = gate_of<kLogNone>(g2, b2, r2, &f); break;
-    default: a = gate_of<kLogComplement>(g2, b2, r2, &f); break;
+    case kDtNone: y = step<kDtNone>(gv, bias, nrate2, xv, h0); break;
+    case kDtDt: y = step<kDtDt>(gv, bias, nrate2, xv, h0); break;
+    case kDtComplement: y = step<kDtComplement>(gv, bias, nrate2, xv, h0); break;
+    case kLogNone: y = step<kLogNone>(gv, bias, nrate2, xv, h0); break;
+    default: y = step<kLogComplement>(gv, bias, nrate2, xv, h0); break;
     }
-    const float y = fmaf(a.x, h0, f.x * xv);
     g.h_out[i] = y;
     store_one(static_cast<T *>(g.out.ptr) + b * g.out.stride_b + h * g.out.stride_h + j, y);
 }

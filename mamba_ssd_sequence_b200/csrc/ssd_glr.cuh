@@ -18,6 +18,7 @@ namespace ssd {
 namespace glr {
 
 constexpr int kSeg = SSD_GLR_CHUNK;  // tokens per thread and per saved state
+constexpr int kMaxCluster = 8;
 
 struct Args {
     ssd_view x, gate, out, dy, dx, dgate;
@@ -95,40 +96,52 @@ __device__ __forceinline__ void store_pair(float *p, float2 v) { *reinterpret_ca
 __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 v) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
+// Two fp32 values in the places of a thread's own x and gate of a token, once
+// it has read those: registers are scarcer than shared memory here.
+__device__ __forceinline__ void keep_pair(float *x, float *, float2 v) { store_pair(x, v); }
+__device__ __forceinline__ float2 kept_pair(const float *x, const float *) { return load_pair(x); }
+__device__ __forceinline__ void keep_pair(__nv_bfloat16 *x, __nv_bfloat16 *gate, float2 v) {
+    *reinterpret_cast<float *>(x) = v.x;
+    *reinterpret_cast<float *>(gate) = v.y;
+}
+__device__ __forceinline__ float2 kept_pair(const __nv_bfloat16 *x, const __nv_bfloat16 *gate) {
+    return make_float2(*reinterpret_cast<const float *>(x), *reinterpret_cast<const float *>(gate));
+}
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ float minus_infinity() { return __uint_as_float(0xFF800000u); }
 
-// q(t) of 1 - exp(-t) = t q(t) for |t| < 1/2 (coefficients from
+// q of exp(s) = 1 + s q(s) for |s| < 1/2 (1 - exp(-t) = t q(-t): coefficients from
 // mamba_ssd_sequence_b200/gen_decay_poly.py, relative error 2.1e-7).
-__device__ __forceinline__ float2 decay_poly(float2 t) {
-    float2 p = both(-1.398218563e-03f);
-    p = fma2(p, t, both(8.408029564e-03f));
-    p = fma2(p, t, both(-4.166579247e-02f));
-    p = fma2(p, t, both(1.666596532e-01f));
-    p = fma2(p, t, both(-5.000000000e-01f));
-    return fma2(p, t, both(1.000000119e+00f));
+__device__ __forceinline__ float2 decay_poly(float2 s) {
+    float2 p = both(1.398218563e-03f);
+    p = fma2(p, s, both(8.408029564e-03f));
+    p = fma2(p, s, both(4.166579247e-02f));
+    p = fma2(p, s, both(1.666596532e-01f));
+    p = fma2(p, s, both(5.000000000e-01f));
+    return fma2(p, s, both(1.000000119e+00f));
 }
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y)); }
 
-// a = exp(-t) and 1 - a.  Near t = 0 the hardware exponential's error (2^-22)
-// would have one sign over the many tokens that a slow decay spans, and add
-// up; 1 - t q(t) is rounded once, either way, and its 1 - a is exact to its
-// last bits.
-__device__ __forceinline__ float2 decay_of(float2 t, float2 *one_minus) {
-    const float2 q = decay_poly(t), w = mul2(t, q), c = fma2(neg2(t), q, both(1.0f));
-    const float2 e = make_float2(ptx::ex2_approx(t.x * -1.4426950408889634f), ptx::ex2_approx(t.y * -1.4426950408889634f));
-    const bool sx = fabsf(t.x) < 0.5f, sy = fabsf(t.y) < 0.5f;
-    *one_minus = make_float2(sx ? w.x : 1.0f - e.x, sy ? w.y : 1.0f - e.y);
+// a = 2^l.  The hardware exponential is off by 1.4e-7 at most, but by -2e-8 on
+// the mean (measured over l in [-0.5, 0]), which adds up over the many tokens
+// that a slow decay spans.  So a segment's product of decays is evaluated
+// from the sum of its l, near 1 by the polynomial (decay_of), and the
+// hardware's error acts within a segment only.
+__device__ __forceinline__ float2 exact_decay(float2 l, float2 *one_minus) {
+    const float2 la = mul2(l, both(0.6931471806f)), q = decay_poly(la), e = ex2(l);
+    const float2 c = fma2(la, q, both(1.0f)), w = mul2(la, q);
+    const bool sx = fabsf(la.x) < 0.5f, sy = fabsf(la.y) < 0.5f;
+    *one_minus = make_float2(sx ? -w.x : 1.0f - e.x, sy ? -w.y : 1.0f - e.y);
     return make_float2(sx ? c.x : e.x, sy ? c.y : e.y);
 }
 
-// dt = softplus(p) = max(p, 0) + log1p(exp(-|p|)), the polynomial of
-// softplus_fast (ssd_math.cuh); u receives exp(-|p|).
+// dt = softplus(p) = max(p, 0) + log1p(u), u = exp(-|p|), with the polynomial
+// of softplus_fast (ssd_math.cuh).
 __device__ __forceinline__ float2 softplus2(float2 p, float2 *u_out) {
-    const float2 u = make_float2(ptx::ex2_approx(-fabsf(p.x) * 1.4426950408889634f),
-                                 ptx::ex2_approx(-fabsf(p.y) * 1.4426950408889634f));
+    const float2 u = ex2(make_float2(-fabsf(p.x) * 1.4426950408889634f, -fabsf(p.y) * 1.4426950408889634f));
     float2 q = both(5.126102362e-03f);
     q = fma2(q, u, both(-2.907406539e-02f));
     q = fma2(q, u, both(7.751608640e-02f));
@@ -141,24 +154,47 @@ __device__ __forceinline__ float2 softplus2(float2 p, float2 *u_out) {
     *u_out = u;
     return fma2(u, q, make_float2(fmaxf(p.x, 0.0f), fmaxf(p.y, 0.0f)));
 }
-// d dt / d p = sigmoid(p), from u = exp(-|p|)
-__device__ __forceinline__ float slope_of(float p, float u) {
-    return __fdividef(p >= 0.0f ? 1.0f : u, 1.0f + u);
-}
 
-// One token of two channels: the decay a, the factor f of x.
+// One token of two channels.
+struct Gate {
+    float2 l;      // log2 a
+    float2 a, f;   // the decay, the factor of x (f = 1 is not used)
+    float2 p, u;   // softplus gates: gate + bias, exp(-|p|)
+};
+
+// nrate2 = -exp(A_log) log2(e).  The logarithm is kept finite, so that its
+// product with a = 0 is 0.
 template <int kMode>
-__device__ __forceinline__ float2 gate_of(float2 g, float2 bias, float2 rate, float2 *f) {
-    float2 w, s = both(0.0f), t, u;
-    if (ModeOf<kMode>::log) {
-        t = neg2(g);
+__device__ __forceinline__ Gate gate_of(float2 g, float2 bias, float2 nrate2) {
+    using M = ModeOf<kMode>;
+    Gate o;
+    if (M::log) {
+        o.l = mul2(g, both(1.4426950408889634f));
     } else {
-        s = softplus2(add2(g, bias), &u);
-        t = mul2(rate, s);
+        o.p = add2(g, bias);
+        o.f = softplus2(o.p, &o.u);
+        o.l = mul2(nrate2, o.f);
     }
-    const float2 a = decay_of(t, &w);
-    *f = ModeOf<kMode>::dt ? s : ModeOf<kMode>::complement ? w : both(1.0f);
-    return a;
+    if (M::complement)
+        o.a = exact_decay(o.l, &o.f);
+    else
+        o.a = ex2(o.l);
+    return o;
+}
+// f x
+template <int kMode>
+__device__ __forceinline__ float2 value_of(const Gate &o, float2 x) {
+    return kMode == kDtNone || kMode == kLogNone ? x : mul2(o.f, x);
+}
+// d dt / d p = sigmoid(p)
+__device__ __forceinline__ float2 slope_of(const Gate &o) {
+    const float2 v = add2(both(1.0f), o.u);
+    return make_float2(__fdividef(o.p.x >= 0.0f ? 1.0f : o.u.x, v.x), __fdividef(o.p.y >= 0.0f ? 1.0f : o.u.y, v.y));
+}
+// the map of a segment from the sum of its log2 a
+__device__ __forceinline__ float2 segment_decay(float2 sum) {
+    float2 w;
+    return exact_decay(sum, &w);
 }
 
 __device__ __forceinline__ int length_of(const int *lengths, int b, int N) {
@@ -236,16 +272,16 @@ __device__ __forceinline__ void close_gates(T *col, int valid) {
         store_pair(col + k * kCb, make_float2(minus_infinity(), minus_infinity()));
 }
 
-// (A, h) of two channels: the map h_in -> A h_in + h over a span of tokens,
-// as {A0, h0, A1, h1}.  then(p, q): p's span, and q's after it in the
-// direction of the scan.
-__device__ __forceinline__ float4 then(float4 p, float4 q) {
-    return make_float4(p.x * q.x, fmaf(q.x, p.y, q.y), p.z * q.z, fmaf(q.z, p.w, q.w));
-}
-__device__ __forceinline__ float4 identity_map() { return make_float4(1.0f, 0.0f, 1.0f, 0.0f); }
+// The map h_in -> A h_in + h of two channels over a span of tokens, as {A0, A1,
+// h0, h1}.  then(p, q): p's span, and q's after it in the direction of the scan.
+__device__ __forceinline__ float4 make_map(float2 A, float2 h) { return make_float4(A.x, A.y, h.x, h.y); }
 __device__ __forceinline__ float2 apply(float4 m, float2 h) {
-    return make_float2(fmaf(m.x, h.x, m.y), fmaf(m.z, h.y, m.w));
+    return fma2(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
 }
+__device__ __forceinline__ float4 then(float4 p, float4 q) {
+    return make_map(mul2(make_float2(p.x, p.y), make_float2(q.x, q.y)), apply(q, make_float2(p.z, p.w)));
+}
+__device__ __forceinline__ float4 identity_map() { return make_float4(1.0f, 1.0f, 0.0f, 0.0f); }
 template <bool kUp>
 __device__ __forceinline__ float4 shift(float4 m, int n) {
     float4 r;
@@ -267,7 +303,7 @@ __device__ __forceinline__ float4 shift(float4 m, int n) {
 template <int kLanes, int kWarps>
 struct Maps {
     float4 warp[kWarps][kLanes];
-    float4 tile[2][8][kLanes];
+    float4 tile[2][kMaxCluster][kLanes];
     uint64_t bar[2];
 };
 template <typename T, int kCb>
@@ -313,29 +349,33 @@ __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, MapsO
     }
     if (in_warp == (kForward ? Tl::per_warp - 1 : 0)) maps->warp[warp][lane] = upto;
     __syncthreads();
-    // the threads of the tile's last segment join the tile's map
+    if (cluster == 1) {  // every thread joins the tile's map for itself
+        float4 base = identity_map(), all = identity_map();
+#pragma unroll
+        for (int i = 0; i < Tl::warps; ++i) {
+            const int w = kForward ? i : Tl::warps - 1 - i;
+            const float4 m = maps->warp[w][lane];
+            if (w == warp) base = all;
+            all = i == 0 ? m : then(all, m);
+        }
+        const float2 h = apply(base, carry);
+        carry = apply(all, carry);
+        return Tl::per_warp > 1 ? apply(before, h) : h;
+    }
+    // the threads of the tile's last segment join and send the tile's map
     const int two = round & 1;
     if (warp == (kForward ? Tl::warps - 1 : 0) && in_warp == (kForward ? Tl::per_warp - 1 : 0)) {
         float4 all = maps->warp[kForward ? 0 : Tl::warps - 1][lane];
 #pragma unroll
         for (int i = 1; i < Tl::warps - 1; ++i) all = then(all, maps->warp[kForward ? i : Tl::warps - 1 - i][lane]);
         all = then(all, upto);
-        float4 *slot = &maps->tile[two][rank][lane];
-        if (cluster == 1) {
-            *slot = all;
-        } else {
-            const uint32_t at = ptx::smem_u32(slot), bar = ptx::smem_u32(&maps->bar[two]);
-            for (int r = 0; r < cluster; ++r) st_async_f4(ptx::mapa_shared(at, r), ptx::mapa_shared(bar, r), all);
-        }
+        const uint32_t at = ptx::smem_u32(&maps->tile[two][rank][lane]), bar = ptx::smem_u32(&maps->bar[two]);
+        for (int r = 0; r < cluster; ++r) st_async_f4(ptx::mapa_shared(at, r), ptx::mapa_shared(bar, r), all);
     }
-    if (cluster == 1) {
-        __syncthreads();
-    } else {
-        if (!lost) lost = !ptx::mbar_wait_cluster(&maps->bar[two], (round >> 1) & 1);
-        if (lost) carry = both(__uint_as_float(0x7FC00000u));
-        // every thread waits for this phase itself; the next one's bytes are announced here
-        if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&maps->bar[two], (uint32_t)cluster * sizeof(maps->tile[0][0]));
-    }
+    if (!lost) lost = !ptx::mbar_wait_cluster(&maps->bar[two], (round >> 1) & 1);
+    if (lost) carry = both(__uint_as_float(0x7FC00000u));
+    // every thread waits for this phase itself; the next one's bytes are announced here
+    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&maps->bar[two], (uint32_t)cluster * sizeof(maps->tile[0][0]));
     float2 h = carry;
     for (int i = 0; i < cluster; ++i) {
         const int r = kForward ? i : cluster - 1 - i;

@@ -6,10 +6,9 @@
 // per thread segment, restart h without a second scan, so a round reads x, the
 // gate and dy once and writes dx and dgate once.
 //
-// A thread keeps a and a h_{t-1} of its 16 tokens in registers while the maps
-// of the adjoint are joined; the softplus and its slope are evaluated again
-// afterwards from the tile in shared memory, which costs less than the
-// registers that would hold them.
+// A thread reduces its 16 tokens to three numbers each before the maps of the
+// adjoint are joined: two in registers, one in the place of x and the gate in
+// shared memory.  The second walk, which has l, is a handful of products.
 //
 // Bound by HBM: 10 bytes an element in bf16, 20 in fp32, and the states (0.25).
 #include "ssd_glr.cuh"
@@ -20,6 +19,15 @@ namespace glr {
 namespace {
 
 constexpr int kStages = 2;
+
+// a and 1 - a of a decay a <= 1 in one number: 1 - a where that is below 1/2, else
+// -a; so each keeps its own relative precision.
+__device__ __forceinline__ float pack_decay(float a, float w) { return w < 0.5f ? w : -a; }
+__device__ __forceinline__ void unpack_decay(float c, float &a, float &w) {
+    const bool is_a = __float_as_int(c) < 0;  // -0 too
+    a = is_a ? -c : 1.0f - c;
+    w = is_a ? 1.0f + c : c;
+}
 
 template <typename T, int kCb>
 constexpr size_t smem_bytes() {
@@ -75,10 +83,11 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
     float2 next_state = state_at(0);
 
-    float2 rate = make_float2(1.0f, 1.0f), bias = make_float2(0.0f, 0.0f), carry = make_float2(0.0f, 0.0f);
+    constexpr float log2e = 1.4426950408889634f;
+    float2 nrate2 = both(-log2e), bias = make_float2(0.0f, 0.0f), carry = make_float2(0.0f, 0.0f);
     const long long pc = (long long)h * g.d + c, bc = (long long)b * g.H * g.d + pc;
     if (!M::log) {
-        if (g.A_log) rate = make_float2(on0 ? expf(g.A_log[pc]) : 1.0f, on1 ? expf(g.A_log[pc + 1]) : 1.0f);
+        if (g.A_log) nrate2 = make_float2(on0 ? -log2e * expf(g.A_log[pc]) : 0.0f, on1 ? -log2e * expf(g.A_log[pc + 1]) : 0.0f);
         if (g.dt_bias) bias = make_float2(on0 ? g.dt_bias[pc] : 0.0f, on1 ? g.dt_bias[pc + 1] : 0.0f);
     }
     if (g.dh_out) carry = make_float2(on0 ? g.dh_out[bc] : 0.0f, on1 ? g.dh_out[bc + 1] : 0.0f);
@@ -94,6 +103,8 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
         }
     };
     float2 sumA = make_float2(0.0f, 0.0f), sumb = make_float2(0.0f, 0.0f);
+    const float2 nrate = mul2(nrate2, both(0.6931471806f));
+    const float2 inv_nrate2 = make_float2(1.0f / nrate2.x, 1.0f / nrate2.y);
 
     init_maps(maps, (int)cluster);
     bool lost = false;
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
         __syncthreads();  // this round has arrived for every thread, and the one before it is consumed
         fetch(i + kStages - 1);
         unsigned char *st = sm + (i % kStages) * 3 * Tl::bytes;
-        const T *xc = own_column<T, kCb>(st);
+        T *xc = own_column<T, kCb>(st);
         T *gc = own_column<T, kCb>(st + Tl::bytes);
         const T *yc = own_column<T, kCb>(st + 2 * Tl::bytes);
         const long long t0 = first_token(i) + seg * kSeg;
@@ -110,55 +121,62 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
         if (!M::log && valid < kSeg) close_gates<T, kCb>(gc, valid);
         float2 hs = next_state;
         next_state = state_at(i + 1);
-        // a, and q = a h_{t-1} (a (h_{t-1} - x) for f = 1 - a): d log a = l q
-        float2 a[kSeg], q[kSeg];
-        float2 prod = both(1.0f), first = both(0.0f);  // l behind the segment -> a_0 l_0
+        // With q = a h_{t-1} (a (h_{t-1} - x) for f = 1 - a), d log a = l q.  All
+        // that the second walk needs but l goes into three numbers a token:
+        //   c   a, or for f = dt log2 a, or for f = 1 - a one of 1 - a and -a
+        //   r   dgate / l
+        //   z   softplus gates: d A_log's term / l; log-decays: f = 1 - a
+        float2 c[kSeg], r[kSeg], sum = both(0.0f), decay = both(1.0f), first = both(0.0f);  // l behind -> a_0 l_0
 #pragma unroll
         for (int k = 0; k < kSeg; ++k) {
-            const float2 xv = load_pair(xc + k * kCb), gv = load_pair(gc + k * kCb), yv = load_pair(yc + k * kCb);
-            float2 f;
-            a[k] = gate_of<kMode>(gv, bias, rate, &f);
-            const float2 ah = mul2(a[k], hs);
-            q[k] = M::complement ? fma2(neg2(a[k]), xv, ah) : ah;
-            hs = kMode == kDtNone || kMode == kLogNone ? add2(ah, xv) : fma2(f, xv, ah);
-            prod = mul2(prod, a[k]);
-            first = fma2(prod, yv, first);
+            const float2 xv = load_pair(xc + k * kCb), yv = load_pair(yc + k * kCb);
+            const Gate o = gate_of<kMode>(load_pair(gc + k * kCb), bias, nrate2);
+            const float2 q = mul2(o.a, M::complement ? add2(hs, neg2(xv)) : hs);
+            hs = fma2(o.a, hs, value_of<kMode>(o, xv));
+            sum = add2(sum, o.l);
+            decay = mul2(decay, o.a);
+            first = fma2(decay, yv, first);
+            c[k] = M::dt ? o.l : o.a;
+            if (M::log) {
+                r[k] = q;
+                if (M::complement) keep_pair(xc + k * kCb, gc + k * kCb, o.f);
+            } else {
+                if (M::complement) c[k] = make_float2(pack_decay(o.a.x, o.f.x), pack_decay(o.a.y, o.f.y));
+                r[k] = mul2(slope_of(o), M::dt ? fma2(nrate, q, xv) : mul2(nrate, q));
+                keep_pair(xc + k * kCb, gc + k * kCb,
+                          mul2(q, make_float2(fmaxf(o.l.x, -3.0e38f), fmaxf(o.l.y, -3.0e38f))));
+            }
         }
-        const float4 own = make_float4(prod.x, first.x, prod.y, first.y);
+        const float4 own = make_map(segment_decay(sum), first);
         float2 lc = enter_segment<T, kCb, false>(own, carry, maps, i, rank, (int)cluster, lost);
+        if (M::dt) {  // a is evaluated again: kept from above it would take the registers back
+#pragma unroll
+            for (int k = 0; k < kSeg; ++k) asm volatile("" : "+f"(c[k].x), "+f"(c[k].y));
+        }
         float2 segA = both(0.0f), segb = both(0.0f);
         // token k: the gradients of x and the gate
         auto token = [&](int k, float2 *vx, float2 *vg) {
-            const float2 yv = load_pair(yc + k * kCb);
-            const float2 l = add2(lc, yv);
-            lc = mul2(a[k], l);
-            const float2 dla = mul2(l, q[k]);
-            if (M::log) {
-                *vg = dla;
-                *vx = l;
-                if (M::complement) {
-                    float2 w;
-                    (void)decay_of(neg2(load_pair(gc + k * kCb)), &w);
-                    *vx = mul2(w, l);
-                }
-                return;
-            }
-            float2 u;
-            const float2 p = add2(load_pair(gc + k * kCb), bias), s = softplus2(p, &u), t = mul2(rate, s);
-            float2 ds = mul2(neg2(rate), dla);
+            const float2 l = add2(lc, load_pair(yc + k * kCb));
+            const float2 z = M::log && !M::complement ? both(1.0f) : kept_pair(xc + k * kCb, gc + k * kCb);
             *vx = l;
+            *vg = mul2(l, r[k]);
+            float2 a = c[k];
             if (M::dt) {
-                *vx = mul2(s, l);
-                ds = fma2(l, load_pair(xc + k * kCb), ds);
+                a = ex2(c[k]);
+                *vx = mul2(mul2(c[k], inv_nrate2), l);
             }
-            if (M::complement) {
-                const float2 w = mul2(t, decay_poly(t));
-                *vx = mul2(make_float2(fabsf(t.x) < 0.5f ? w.x : 1.0f - a[k].x, fabsf(t.y) < 0.5f ? w.y : 1.0f - a[k].y), l);
+            if (M::complement && !M::log) {
+                float2 f;
+                unpack_decay(c[k].x, a.x, f.x);
+                unpack_decay(c[k].y, a.y, f.y);
+                *vx = mul2(f, l);
             }
-            *vg = mul2(ds, make_float2(slope_of(p.x, u.x), slope_of(p.y, u.y)));
-            // where a = 0 log a may be -infinity, and the product is 0
-            segA = fma2(neg2(dla), make_float2(fminf(t.x, 200.0f), fminf(t.y, 200.0f)), segA);
-            segb = add2(segb, *vg);
+            if (M::complement && M::log) *vx = mul2(z, l);
+            lc = mul2(a, l);
+            if (!M::log) {
+                segA = fma2(l, z, segA);
+                segb = add2(segb, *vg);
+            }
         };
         if (g.aligned && valid == kSeg) {
             T *ox = dx + (t0 + kSeg - 1) * g.dx.stride_n, *og = dgate + (t0 + kSeg - 1) * g.dgate.stride_n;
@@ -202,7 +220,8 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
     if (!M::log && g.part) {
         __syncthreads();
         float4 *sums = reinterpret_cast<float4 *>(sm);
-        sums[threadIdx.x] = make_float4(sumA.x, sumb.x, sumA.y, sumb.y);
+        constexpr float ln2 = 0.6931471806f;  // the terms are in units of log2 a
+        sums[threadIdx.x] = make_float4(ln2 * sumA.x, sumb.x, ln2 * sumA.y, sumb.y);
         __syncthreads();
         if (seg == 0) {
             float4 v = sums[lane];

@@ -2,11 +2,11 @@
 //
 // A cluster takes one block of channels through its sequence in rounds of
 // cluster x tile tokens.  In a round each thread evaluates the gates of its
-// 16-token segment once, keeps a and f x in registers, and reduces them to the
-// segment's map h_in -> A h_in + h; the maps are joined over the segments of a
+// 16-token segment once, keeps a in registers and f x in the place of x and the
+// gate in shared memory, and reduces them to the segment's map h_in -> A h_in + h; the maps are joined over the segments of a
 // warp (shuffles), the warps of a block (shared memory) and the blocks of the
 // cluster (distributed shared memory), which gives each segment its h_in; a
-// second walk over the registers then gives h.  So x and the gate are read and
+// second walk then gives h.  So x and the gate are read and
 // h is written once, whatever the number of channels.
 //
 // Bound by HBM: 6 bytes an element in bf16, 12 in fp32.
@@ -17,7 +17,7 @@ namespace ssd {
 namespace glr {
 namespace {
 
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 
 template <typename T, int kCb>
 constexpr size_t smem_bytes() {
@@ -29,6 +29,7 @@ template <typename T, int kCb, int kMode>
 __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g) {
     using Tl = Tile<T, kCb>;
     using M = ModeOf<kMode>;
+    constexpr bool kPlain = kMode == kDtNone || kMode == kLogNone;  // f x is x
     extern __shared__ __align__(128) unsigned char sm[];
     auto *maps = reinterpret_cast<MapsOf<T, kCb> *>(sm + kStages * 2 * Tl::bytes);
 
@@ -58,10 +59,11 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
 #pragma unroll
     for (int r = 0; r < kStages - 1; ++r) fetch(r);
 
-    float2 rate = make_float2(1.0f, 1.0f), bias = make_float2(0.0f, 0.0f), carry = make_float2(0.0f, 0.0f);
+    constexpr float log2e = 1.4426950408889634f;
+    float2 nrate2 = both(-log2e), bias = make_float2(0.0f, 0.0f), carry = make_float2(0.0f, 0.0f);
     const long long pc = (long long)h * g.d + c, bc = (long long)b * g.H * g.d + pc;
     if (!M::log) {
-        if (g.A_log) rate = make_float2(on0 ? expf(g.A_log[pc]) : 1.0f, on1 ? expf(g.A_log[pc + 1]) : 1.0f);
+        if (g.A_log) nrate2 = make_float2(on0 ? -log2e * expf(g.A_log[pc]) : 0.0f, on1 ? -log2e * expf(g.A_log[pc + 1]) : 0.0f);
         if (g.dt_bias) bias = make_float2(on0 ? g.dt_bias[pc] : 0.0f, on1 ? g.dt_bias[pc + 1] : 0.0f);
     }
     if (g.h0) carry = make_float2(on0 ? g.h0[bc] : 0.0f, on1 ? g.h0[bc + 1] : 0.0f);
@@ -90,23 +92,24 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         __syncthreads();  // round r has arrived for every thread, and round r - 1 is consumed
         fetch(r + kStages - 1);
         unsigned char *st = sm + (r % kStages) * 2 * Tl::bytes;
-        const T *xc = own_column<T, kCb>(st);
+        T *xc = own_column<T, kCb>(st);
         T *gc = own_column<T, kCb>(st + Tl::bytes);
         const long long t0 = r * round_tok + (long long)rank * Tl::tok + seg * kSeg;
         const int valid = (int)max(0ll, min((long long)kSeg, len - t0));
         if (!M::log && valid < kSeg) close_gates<T, kCb>(gc, valid);
-        float2 a[kSeg], u[kSeg];
-        float2 prod = both(1.0f), end = both(0.0f);
+        float2 a[kSeg], sum = both(0.0f), end = both(0.0f);
 #pragma unroll
         for (int k = 0; k < kSeg; ++k) {
-            const float2 xv = load_pair(xc + k * kCb), gv = load_pair(gc + k * kCb);
-            float2 f;
-            a[k] = gate_of<kMode>(gv, bias, rate, &f);
-            u[k] = kMode == kDtNone || kMode == kLogNone ? xv : mul2(f, xv);
-            prod = mul2(prod, a[k]);
-            end = fma2(a[k], end, u[k]);
+            const float2 xv = load_pair(xc + k * kCb);
+            const Gate o = gate_of<kMode>(load_pair(gc + k * kCb), bias, nrate2);
+            const float2 u = value_of<kMode>(o, xv);
+            a[k] = o.a;
+            sum = add2(sum, o.l);
+            end = fma2(o.a, end, u);
+            if (!kPlain) keep_pair(xc + k * kCb, gc + k * kCb, u);
         }
-        const float4 own = make_float4(prod.x, end.x, prod.y, end.y);
+        auto value = [&](int k) { return kPlain ? load_pair(xc + k * kCb) : kept_pair(xc + k * kCb, gc + k * kCb); };
+        const float4 own = make_map(segment_decay(sum), end);
         float2 hs = enter_segment<T, kCb, true>(own, carry, maps, r, rank, (int)cluster, lost);
         if (states && t0 < g.N) save(t0 / kSeg, hs);
         if (g.aligned && valid == kSeg) {
@@ -114,14 +117,14 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
                 T *o = out + t0 * g.out.stride_n;
 #pragma unroll
                 for (int k = 0; k < kSeg; ++k, o += g.out.stride_n) {
-                    hs = fma2(a[k], hs, u[k]);
+                    hs = fma2(a[k], hs, value(k));
                     store_pair(o, hs);
                 }
             }
         } else {
 #pragma unroll
             for (int k = 0; k < kSeg; ++k) {
-                hs = fma2(a[k], hs, u[k]);
+                hs = fma2(a[k], hs, value(k));
                 if (t0 + k < g.N) store(t0 + k, k < valid ? hs : both(0.0f));
             }
         }

@@ -2,7 +2,6 @@
 // ssd_glr_step), the cut of a call into clusters, the decode step and the sums
 // of the parameter gradients.
 #include "ssd_glr.cuh"
-#include "ssd_internal.h"
 
 namespace ssd {
 namespace glr {

@@ -10,7 +10,10 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "ptx.cuh"
+#include "ssd_internal.h"
 #include "ssd_math.cuh"
 #include "ssd_view.h"
 
@@ -401,10 +404,17 @@ Cut cut_of(int B, int H, int N, int d, int dtype);
 int launch_fwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s);
 int launch_bwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s);
 
-template <typename K>
-int launch_cluster(K kernel, const Args &g, const Cut &p, int threads, size_t smem, cudaStream_t s) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return SSD_ERR_CUDA;
+// Launches a kernel in clusters.  Its shared memory limit is set once per CUDA
+// context (the driver never reuses a context's ID).
+template <auto kernel>
+int launch_cluster(const Args &g, const Cut &p, int threads, size_t smem, cudaStream_t s) {
+    static std::atomic<unsigned long long> set_in{0};
+    unsigned long long id = 0;
+    if (!current_context_id(&id) || set_in.load(std::memory_order_relaxed) != id + 1) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return SSD_ERR_CUDA;
+        if (id) set_in.store(id + 1, std::memory_order_relaxed);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)p.cluster;

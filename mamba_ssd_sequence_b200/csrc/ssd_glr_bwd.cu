@@ -12,7 +12,6 @@
 //
 // Bound by HBM: 10 bytes an element in bf16, 20 in fp32, and the states (0.25).
 #include "ssd_glr.cuh"
-#include "ssd_internal.h"
 
 namespace ssd {
 namespace glr {
@@ -243,11 +242,11 @@ int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
     constexpr size_t sm = smem_bytes<T, kCb>();
     constexpr int nt = Threads<T>::n;
     switch (mode) {
-    case kDtNone: return launch_cluster(glr_bwd_kernel<T, kCb, kDtNone>, g, p, nt, sm, s);
-    case kDtDt: return launch_cluster(glr_bwd_kernel<T, kCb, kDtDt>, g, p, nt, sm, s);
-    case kDtComplement: return launch_cluster(glr_bwd_kernel<T, kCb, kDtComplement>, g, p, nt, sm, s);
-    case kLogNone: return launch_cluster(glr_bwd_kernel<T, kCb, kLogNone>, g, p, nt, sm, s);
-    default: return launch_cluster(glr_bwd_kernel<T, kCb, kLogComplement>, g, p, nt, sm, s);
+    case kDtNone: return launch_cluster<glr_bwd_kernel<T, kCb, kDtNone>>(g, p, nt, sm, s);
+    case kDtDt: return launch_cluster<glr_bwd_kernel<T, kCb, kDtDt>>(g, p, nt, sm, s);
+    case kDtComplement: return launch_cluster<glr_bwd_kernel<T, kCb, kDtComplement>>(g, p, nt, sm, s);
+    case kLogNone: return launch_cluster<glr_bwd_kernel<T, kCb, kLogNone>>(g, p, nt, sm, s);
+    default: return launch_cluster<glr_bwd_kernel<T, kCb, kLogComplement>>(g, p, nt, sm, s);
     }
 }
 

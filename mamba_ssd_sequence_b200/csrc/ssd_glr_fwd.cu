@@ -11,7 +11,6 @@
 //
 // Bound by HBM: 6 bytes an element in bf16, 12 in fp32.
 #include "ssd_glr.cuh"
-#include "ssd_internal.h"
 
 namespace ssd {
 namespace glr {
@@ -149,11 +148,11 @@ int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
     constexpr size_t sm = smem_bytes<T, kCb>();
     constexpr int nt = Threads<T>::n;
     switch (mode) {
-    case kDtNone: return launch_cluster(glr_fwd_kernel<T, kCb, kDtNone>, g, p, nt, sm, s);
-    case kDtDt: return launch_cluster(glr_fwd_kernel<T, kCb, kDtDt>, g, p, nt, sm, s);
-    case kDtComplement: return launch_cluster(glr_fwd_kernel<T, kCb, kDtComplement>, g, p, nt, sm, s);
-    case kLogNone: return launch_cluster(glr_fwd_kernel<T, kCb, kLogNone>, g, p, nt, sm, s);
-    default: return launch_cluster(glr_fwd_kernel<T, kCb, kLogComplement>, g, p, nt, sm, s);
+    case kDtNone: return launch_cluster<glr_fwd_kernel<T, kCb, kDtNone>>(g, p, nt, sm, s);
+    case kDtDt: return launch_cluster<glr_fwd_kernel<T, kCb, kDtDt>>(g, p, nt, sm, s);
+    case kDtComplement: return launch_cluster<glr_fwd_kernel<T, kCb, kDtComplement>>(g, p, nt, sm, s);
+    case kLogNone: return launch_cluster<glr_fwd_kernel<T, kCb, kLogNone>>(g, p, nt, sm, s);
+    default: return launch_cluster<glr_fwd_kernel<T, kCb, kLogComplement>>(g, p, nt, sm, s);
     }
 }
 

@@ -201,6 +201,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// 1 / x within 1 ulp; 0 for infinity (and beyond 2^126)
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // --------------------------------------------------------------- async proxy
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

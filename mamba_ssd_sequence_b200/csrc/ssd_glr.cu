@@ -1,6 +1,5 @@
 // Gated linear recurrence: entry points (ssd.h, ssd_glr_fwd / ssd_glr_bwd /
-// ssd_glr_step), the cut of a call into clusters, the decode step and the sums
-// of the parameter gradients.
+// ssd_glr_step), the cut of a call into clusters, and the decode step.
 #include "ssd_glr.cuh"
 
 namespace ssd {
@@ -55,20 +54,6 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(const Args g, int mo
     }
     g.h_out[i] = y;
     store_one(static_cast<T *>(g.out.ptr) + b * g.out.stride_b + h * g.out.stride_h + j, y);
-}
-
-// dA_log and ddt_bias: sums over the batch and the blocks of a cluster, in order.
-__global__ void __launch_bounds__(kThreads)
-glr_param_kernel(const float2 *part, int rows, long long C, float *dA, float *db) {
-    const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= C) return;
-    float2 s = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < rows; ++i) {
-        const float2 v = part[i * C + c];
-        s.x += v.x, s.y += v.y;
-    }
-    if (dA) dA[c] = s.x;
-    if (db) db[c] = s.y;
 }
 
 unsigned blocks_for(long long n) { return (unsigned)((n + kThreads - 1) / kThreads); }
@@ -184,9 +169,7 @@ int ssd_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     rc = launch_bwd(g, p, dtype, mode_of(flags), s);
     if (rc != SSD_OK || !params) return rc;
-    glr_param_kernel<<<blocks_for(C), kThreads, 0, s>>>(reinterpret_cast<const float2 *>(workspace), B * p.cluster, C,
-                                                        dA_log, ddt_bias);
-    return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    return sum_parts(g.part, (unsigned)(B * p.cluster), 2 * C, (int)C, dA_log, ddt_bias, s);
 }
 
 int ssd_glr_step(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias, int B,

@@ -192,7 +192,8 @@ __device__ __forceinline__ float2 value_of(const Gate &o, float2 x) {
 // d dt / d p = sigmoid(p)
 __device__ __forceinline__ float2 slope_of(const Gate &o) {
     const float2 v = add2(both(1.0f), o.u);
-    return make_float2(__fdividef(o.p.x >= 0.0f ? 1.0f : o.u.x, v.x), __fdividef(o.p.y >= 0.0f ? 1.0f : o.u.y, v.y));
+    return mul2(make_float2(o.p.x >= 0.0f ? 1.0f : o.u.x, o.p.y >= 0.0f ? 1.0f : o.u.y),
+                make_float2(ptx::rcp_approx(v.x), ptx::rcp_approx(v.y)));
 }
 // the map of a segment from the sum of its log2 a
 __device__ __forceinline__ float2 segment_decay(float2 sum) {

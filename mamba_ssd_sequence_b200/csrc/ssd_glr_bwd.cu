@@ -228,9 +228,10 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
                 const float4 o = sums[k * Tl::lanes + lane];
                 v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
             }
-            float2 *part = reinterpret_cast<float2 *>(g.part) + ((long long)b * cluster + rank) * g.H * g.d + pc;
-            if (on0) part[0] = make_float2(v.x, v.y);
-            if (on1) part[1] = make_float2(v.z, v.w);
+            const long long C = (long long)g.H * g.d;
+            float *part = g.part + ((long long)b * cluster + rank) * 2 * C + pc;
+            if (on0) part[0] = v.x, part[C] = v.y;
+            if (on1) part[1] = v.z, part[C + 1] = v.w;
         }
     }
     // no block leaves while a peer may still write to its shared memory

@@ -105,6 +105,11 @@ bool encode_tmap_2d(CUtensorMap *m, const void *base, bool bf16, uint64_t cols, 
 // device's primary context is made current first.  False on a driver error.
 bool current_context_id(unsigned long long *id);
 
+// Sums `rows` rows (of two parameters' C values each, `stride` floats apart) of
+// partial gradients into out0 and out1 (either may be NULL), in a fixed
+// order; a programmatic dependent of the kernel that wrote them (ssd_norm.cu).
+int sum_parts(const float *part, unsigned rows, long long stride, int C, float *out0, float *out1, cudaStream_t s);
+
 // Decode step (ssd_decode.cu).
 size_t decode_workspace(int B, int H, int d, int order);
 int launch_decode(const FwdArgs &a, float *h, float *z);

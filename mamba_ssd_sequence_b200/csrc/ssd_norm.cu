@@ -11,6 +11,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "ptx.cuh"
 #include "ssd_internal.h"
 #include "ssd_view.h"
@@ -422,59 +424,122 @@ __device__ __forceinline__ void store_heads(T *p, long long hop, int j, int d, i
     }
 }
 
+// A thread's own vectors of the rows to come, in shared memory: a ring of kDepth
+// rows of kPer 16-byte pieces a thread, filled by asynchronous copies that take
+// no registers and that only the thread itself waits for.  (Gated norm of 65536 x
+// 2048: 164 us, 196 with one row ahead in registers.  The residual norm moves
+// more per channel, and is faster with registers: 248 us, 323 with a ring.)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+template <int kPer>
+struct Ring {
+    static constexpr int kDepth = kPer <= 8 ? 3 : 2;
+    static constexpr size_t bytes(int threads) { return (size_t)kDepth * kPer * threads * 16; }
+    unsigned char *own;
+    int put, get;
+    __device__ __forceinline__ explicit Ring(void *smem)
+        : own(static_cast<unsigned char *>(smem) + threadIdx.x * 16), put(0), get(0) {}
+    // piece `first` on of the row being put: one vector
+    template <typename T, int kVec>
+    __device__ __forceinline__ void copy(int first, const T *p) {
+#pragma unroll
+        for (int i = 0; i < Raw<T, kVec, true>::n; ++i)
+            copy16(ptx::smem_u32(own + (put * kPer + first + i) * blockDim.x * 16), reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void put_done() {
+        copies_commit();
+        put = put + 1 == kDepth ? 0 : put + 1;
+    }
+    __device__ __forceinline__ void get_wait() { copies_wait<kDepth - 1>(); }
+    template <typename T, int kVec>
+    __device__ __forceinline__ void load(int first, Raw<T, kVec, true> &r) const {
+#pragma unroll
+        for (int i = 0; i < Raw<T, kVec, true>::n; ++i)
+            r.q[i] = *reinterpret_cast<const uint4 *>(own + (get * kPer + first + i) * blockDim.x * 16);
+    }
+    __device__ __forceinline__ void get_done() { get = get + 1 == kDepth ? 0 : get + 1; }
+};
+
+// Rows of at most kThreads threads are fetched ahead through a ring.
+template <bool kAligned, int kMax>
+constexpr bool kRings = kAligned && kMax <= kThreads;
+
 template <typename T, bool kAligned, int kGate, int kNv, int kMax>
-__global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 ? 3 : 2) : 1) gated_norm_kernel(const GatedNormArgs g) {
+__global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 ? 3 : 2) : 1)
+gated_norm_kernel(const GatedNormArgs g) {
     constexpr int kVec = kVecOf<T>;
-    constexpr bool kAhead = kMax == kThreads;  // registers for the next row too
+    constexpr bool kRing = kRings<kAligned, kMax>, has_z = kGate != kNoGate, after = kGate == kGateAfter;
+    extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][32];
     const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr / g.gpb;
     const int group = blockIdx.y * g.gpb + slot % g.gpb, c0 = group * g.L;
     const long long tokens = (long long)g.B * g.N, step = (long long)gridDim.x * slots;
-    constexpr bool has_z = kGate != kNoGate, after = kGate == kGateAfter;
     int h[kNv], j[kNv], left[kNv];
 #pragma unroll
     for (int i = 0; i < kNv; ++i) {
         const int cl = (lane + i * tpr) * kVec;
         h[i] = (c0 + cl) / g.d, j[i] = (c0 + cl) % g.d, left[i] = g.L - cl;
     }
-    Raw<T, kVec, kAligned> xr[kNv], zr[kNv];
-    auto fetch = [&](long long m, const Token &k) {
-        if (m >= tokens) return;
-        const T *x = static_cast<const T *>(g.x.ptr) + k.b * g.x.stride_b + k.n * g.x.stride_n;
-        const T *z = static_cast<const T *>(g.z.ptr) + k.b * g.z.stride_b + k.n * g.z.stride_n;
-#pragma unroll
-        for (int i = 0; i < kNv; ++i)
-            if (left[i] > 0) {
-                load_heads(xr[i], x + h[i] * g.x.stride_h + j[i], g.x.stride_h - g.d, j[i], g.d, left[i]);
-                if (has_z) load_heads(zr[i], z + h[i] * g.z.stride_h + j[i], g.z.stride_h - g.d, j[i], g.d, left[i]);
-            }
-    };
-    long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
+    Ring<2 * kNv> ring(smem);
     const int step_b = (int)(step / g.N), step_n = (int)(step % g.N);
+    long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
     Token here = {(int)(m / g.N), (int)(m % g.N)}, next = here;
-    if (kAhead) fetch(m, here);
+    auto fetch = [&](long long at) {  // of token `next`, which advances
+        if constexpr (kRing) {
+            if (at < tokens) {
+                const T *x = static_cast<const T *>(g.x.ptr) + next.b * g.x.stride_b + next.n * g.x.stride_n;
+                const T *z = static_cast<const T *>(g.z.ptr) + next.b * g.z.stride_b + next.n * g.z.stride_n;
+#pragma unroll
+                for (int i = 0; i < kNv; ++i)
+                    if (left[i] > 0) {
+                        ring.template copy<T, kVec>(i, x + h[i] * g.x.stride_h + j[i]);
+                        if (has_z) ring.template copy<T, kVec>(kNv + i, z + h[i] * g.z.stride_h + j[i]);
+                    }
+            }
+            ring.put_done();
+            next.advance(step_b, step_n, g.N);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k + 1 < ring.kDepth; ++k) fetch(m + k * step);
     int turn = 0;
-    for (; m0 < tokens; m0 += step, m += step, here = next, ++turn) {
-        next.advance(step_b, step_n, g.N);
+    for (; m0 < tokens; m0 += step, m += step, here.advance(step_b, step_n, g.N), ++turn) {
         const bool on = m < tokens;
-        if (!kAhead) fetch(m, here);
+        fetch(m + (ring.kDepth - 1) * step);
+        if (kRing) ring.get_wait();
+        const T *x = static_cast<const T *>(g.x.ptr) + here.b * g.x.stride_b + here.n * g.x.stride_n;
+        const T *z = static_cast<const T *>(g.z.ptr) + here.b * g.z.stride_b + here.n * g.z.stride_n;
         float v[kNv][kVec], ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             if (on && left[i] > 0) {
-                float z[kVec];
-                xr[i].get(v[i]);
-                if (has_z) zr[i].get(z);
+                Raw<T, kVec, kAligned> xr, zr;
+                if constexpr (kRing) {
+                    ring.load(i, xr);
+                    if (has_z) ring.load(kNv + i, zr);
+                } else {
+                    load_heads(xr, x + h[i] * g.x.stride_h + j[i], g.x.stride_h - g.d, j[i], g.d, left[i]);
+                    if (has_z) load_heads(zr, z + h[i] * g.z.stride_h + j[i], g.z.stride_h - g.d, j[i], g.d, left[i]);
+                }
+                float zv[kVec];
+                xr.get(v[i]);
+                if (has_z) zr.get(zv);
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
-                    const float s = has_z ? z[e] * sigmoid<T>(z[e]) : 1.0f;
+                    const float s = has_z ? zv[e] * sigmoid<T>(zv[e]) : 1.0f;
                     const float u = after ? v[i][e] : v[i][e] * s;
                     ss = fmaf(u, u, ss);
                     v[i][e] *= s;
                 }
             }
         }
-        if (kAhead) fetch(m + step, next);
+        ring.get_done();
         const float rs = rsqrtf(row_sum(ss, tpr, red, turn) / g.L + g.eps);
         if (!on) continue;
         T *out = static_cast<T *>(g.out.ptr) + here.b * g.out.stride_b + here.n * g.out.stride_n;
@@ -495,13 +560,12 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 ? 3 :
 template <typename T, bool kAligned, int kGate, int kNv, int kMax>
 __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd_kernel(const GatedNormArgs g) {
     constexpr int kVec = kVecOf<T>;
-    constexpr bool kAhead = kMax == kThreads;  // registers for the next row too
-    extern __shared__ float sh[];
+    constexpr bool kRing = kRings<kAligned, kMax>, has_z = kGate != kNoGate, after = kGate == kGateAfter;
+    extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][32];
     const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr / g.gpb;
     const int group = blockIdx.y * g.gpb + slot % g.gpb, c0 = group * g.L;
     const long long tokens = (long long)g.B * g.N, step = (long long)gridDim.x * slots;
-    constexpr bool has_z = kGate != kNoGate, after = kGate == kGateAfter;
     int h[kNv], j[kNv], left[kNv];
     float dw[kNv][kVec] = {};
 #pragma unroll
@@ -509,41 +573,58 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
         const int cl = (lane + i * tpr) * kVec;
         h[i] = (c0 + cl) / g.d, j[i] = (c0 + cl) % g.d, left[i] = g.L - cl;
     }
-    Raw<T, kVec, kAligned> xr[kNv], zr[kNv], yr[kNv];
-    float rs = 0.0f;
-    auto fetch = [&](long long m, const Token &k) {
-        if (m >= tokens) return;
-        const T *x = static_cast<const T *>(g.x.ptr) + k.b * g.x.stride_b + k.n * g.x.stride_n;
-        const T *z = static_cast<const T *>(g.z.ptr) + k.b * g.z.stride_b + k.n * g.z.stride_n;
-        const T *dy = static_cast<const T *>(g.dy.ptr) + k.b * g.dy.stride_b + k.n * g.dy.stride_n;
-        rs = g.rstd[m * g.groups + group];
-#pragma unroll
-        for (int i = 0; i < kNv; ++i)
-            if (left[i] > 0) {
-                load_heads(xr[i], x + h[i] * g.x.stride_h + j[i], g.x.stride_h - g.d, j[i], g.d, left[i]);
-                load_heads(yr[i], dy + h[i] * g.dy.stride_h + j[i], g.dy.stride_h - g.d, j[i], g.d, left[i]);
-                if (has_z) load_heads(zr[i], z + h[i] * g.z.stride_h + j[i], g.z.stride_h - g.d, j[i], g.d, left[i]);
-            }
-    };
-    long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
+    Ring<3 * kNv> ring(smem);
     const int step_b = (int)(step / g.N), step_n = (int)(step % g.N);
+    long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
     Token here = {(int)(m / g.N), (int)(m % g.N)}, next = here;
-    if (kAhead) fetch(m, here);
+    auto fetch = [&](long long at) {  // of token `next`, which advances
+        if constexpr (kRing) {
+            if (at < tokens) {
+                const T *x = static_cast<const T *>(g.x.ptr) + next.b * g.x.stride_b + next.n * g.x.stride_n;
+                const T *z = static_cast<const T *>(g.z.ptr) + next.b * g.z.stride_b + next.n * g.z.stride_n;
+                const T *dy = static_cast<const T *>(g.dy.ptr) + next.b * g.dy.stride_b + next.n * g.dy.stride_n;
+#pragma unroll
+                for (int i = 0; i < kNv; ++i)
+                    if (left[i] > 0) {
+                        ring.template copy<T, kVec>(i, x + h[i] * g.x.stride_h + j[i]);
+                        ring.template copy<T, kVec>(kNv + i, dy + h[i] * g.dy.stride_h + j[i]);
+                        if (has_z) ring.template copy<T, kVec>(2 * kNv + i, z + h[i] * g.z.stride_h + j[i]);
+                    }
+            }
+            ring.put_done();
+            next.advance(step_b, step_n, g.N);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k + 1 < ring.kDepth; ++k) fetch(m + k * step);
+    float rs_next = m < tokens ? g.rstd[m * g.groups + group] : 0.0f;
     int turn = 0;
-    for (; m0 < tokens; m0 += step, m += step, here = next, ++turn) {
-        next.advance(step_b, step_n, g.N);
+    for (; m0 < tokens; m0 += step, m += step, here.advance(step_b, step_n, g.N), ++turn) {
         const bool on = m < tokens;
-        if (!kAhead) fetch(m, here);
-        const float rsm = rs;
-        // of each channel: xhat, d(normed) = dy (.) w with a gate behind, and
-        // what becomes of them in dx and dz
+        const float rs = rs_next;
+        if (m + step < tokens) rs_next = g.rstd[(m + step) * g.groups + group];
+        fetch(m + (ring.kDepth - 1) * step);
+        if (kRing) ring.get_wait();
+        const T *x = static_cast<const T *>(g.x.ptr) + here.b * g.x.stride_b + here.n * g.x.stride_n;
+        const T *z = static_cast<const T *>(g.z.ptr) + here.b * g.z.stride_b + here.n * g.z.stride_n;
+        const T *dy = static_cast<const T *>(g.dy.ptr) + here.b * g.dy.stride_b + here.n * g.dy.stride_n;
         float xv[kNv][kVec], gy[kNv][kVec], zv[kNv][kVec], sg[kNv][kVec], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             if (on && left[i] > 0) {
-                xr[i].get(xv[i]);
-                yr[i].get(gy[i]);
-                if (has_z) zr[i].get(zv[i]);
+                Raw<T, kVec, kAligned> xr, yr, zr;
+                if constexpr (kRing) {
+                    ring.load(i, xr);
+                    ring.load(kNv + i, yr);
+                    if (has_z) ring.load(2 * kNv + i, zr);
+                } else {
+                    load_heads(xr, x + h[i] * g.x.stride_h + j[i], g.x.stride_h - g.d, j[i], g.d, left[i]);
+                    load_heads(yr, dy + h[i] * g.dy.stride_h + j[i], g.dy.stride_h - g.d, j[i], g.d, left[i]);
+                    if (has_z) load_heads(zr, z + h[i] * g.z.stride_h + j[i], g.z.stride_h - g.d, j[i], g.d, left[i]);
+                }
+                xr.get(xv[i]);
+                yr.get(gy[i]);
+                if (has_z) zr.get(zv[i]);
                 float w[kVec];
                 load_param<kAligned>(g.w, c0 + g.L - left[i], left[i], 1.0f, w);
 #pragma unroll
@@ -551,14 +632,14 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
                     sg[i][e] = has_z ? sigmoid<T>(zv[i][e]) : 1.0f;
                     const float s = has_z ? zv[i][e] * sg[i][e] : 1.0f;
                     // xhat (.) g is the same product in both orders of gate and norm
-                    const float t = gy[i][e] * s * (xv[i][e] * rsm);
+                    const float t = gy[i][e] * s * (xv[i][e] * rs);
                     dw[i][e] += t;
                     gy[i][e] *= w[e];
                     dot = fmaf(t, w[e], dot);
                 }
             }
         }
-        if (kAhead) fetch(m + step, next);
+        ring.get_done();
         dot = row_sum(dot, tpr, red, turn) / g.L;
         if (!on) continue;
         T *dx = static_cast<T *>(g.dx.ptr) + here.b * g.dx.stride_b + here.n * g.dx.stride_n;
@@ -568,26 +649,29 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
             if (left[i] > 0) {
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
-                    const float sig = sg[i][e], s = has_z ? zv[i][e] * sig : 1.0f, x = xv[i][e], gw = gy[i][e];
+                    const float sig = sg[i][e], s = has_z ? zv[i][e] * sig : 1.0f, xx = xv[i][e], gw = gy[i][e];
                     float ds;
                     if (after) {
-                        xv[i][e] = rsm * fmaf(-x * rsm, dot, gw * s);
-                        ds = gw * (x * rsm);
+                        xv[i][e] = rs * fmaf(-xx * rs, dot, gw * s);
+                        ds = gw * (xx * rs);
                     } else {
-                        const float du = rsm * fmaf(-x * s * rsm, dot, gw);
+                        const float du = rs * fmaf(-xx * s * rs, dot, gw);
                         xv[i][e] = du * s;
-                        ds = du * x;
+                        ds = du * xx;
                     }
                     if (has_z) zv[i][e] = ds * sig * fmaf(zv[i][e], 1.0f - sig, 1.0f);
                 }
                 store_heads<kAligned>(dx + h[i] * g.dx.stride_h + j[i], g.dx.stride_h - g.d, j[i], g.d, left[i], xv[i]);
-                if (has_z) store_heads<kAligned>(dz + h[i] * g.dz.stride_h + j[i], g.dz.stride_h - g.d, j[i], g.d, left[i], zv[i]);
+                if (has_z)
+                    store_heads<kAligned>(dz + h[i] * g.dz.stride_h + j[i], g.dz.stride_h - g.d, j[i], g.d, left[i], zv[i]);
             }
         }
     }
-    if (g.part)
-        write_part<kNv, kVec>(dw, sh, slot, slots * g.gpb, lane, tpr, g.gpb, g.L,
+    if (g.part) {
+        copies_wait<0>();
+        write_part<kNv, kVec>(dw, reinterpret_cast<float *>(smem), slot, slots * g.gpb, lane, tpr, g.gpb, g.L,
                               g.part + (long long)blockIdx.x * g.H * g.d + c0);
+    }
 }
 
 // ------------------------------------------------------------------- wide rows
@@ -750,6 +834,7 @@ struct Cut {
 };
 
 constexpr int kSMs = 148;
+constexpr size_t kMaxSmem = 104 * 1024;  // the largest ring: 96 KB
 constexpr unsigned kMaxParts = 4 * kSMs;  // blocks of a backward pass: bounds its workspace
 
 Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward) {
@@ -760,7 +845,7 @@ Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward) {
     while (c.tpr * c.nv < n) c.tpr *= 2;
     c.gpb = 1;
     // rows that need a barrier wait for fewer others in a smaller block (gated norm of 65536 x
-    // 2048: 203 us in blocks of 256, 196 of 128); a gradient's partial sums want large ones
+    // 2048, one row ahead: 203 us in blocks of 256, 196 of 128); a gradient's partial sums want large ones
     c.threads = !backward && c.tpr > 32 ? kThreads / 2 : kThreads;
     if (c.tpr > most) {
         c.nv = 0;
@@ -798,13 +883,29 @@ Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward) {
         }                                                              \
     } while (0)
 
+// Launches a kernel with `smem` bytes of dynamic shared memory, whose limit
+// (48 KB with the static part, unless raised) is
+// set once per CUDA context (the driver never reuses a context's ID).
+template <auto kernel, typename A>
+void launch(dim3 grid, const Cut &c, size_t smem, cudaStream_t s, const A &g) {
+    static std::atomic<unsigned long long> set_in{0};
+    unsigned long long id = 0;
+    if (smem > 40 * 1024 && (!current_context_id(&id) || set_in.load(std::memory_order_relaxed) != id + 1)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
+            return;  // the caller reads the error
+        if (id) set_in.store(id + 1, std::memory_order_relaxed);
+    }
+    kernel<<<grid, c.threads, smem, s>>>(g);
+}
+size_t part_bytes(const Cut &c, int vec) { return (size_t)c.threads * c.nv * vec * sizeof(float); }
+
 template <typename T, typename R>
 void run_add(const AddNormArgs &g, const Cut &c, bool aligned, cudaStream_t s) {
     if (c.nv == 0) {
         add_norm_wide_kernel<T, R><<<c.blocks, kThreads, 0, s>>>(g);
         return;
     }
-#define RUN(AL, NV, MX) add_norm_kernel<T, R, AL, NV, MX><<<c.blocks, c.threads, 0, s>>>(g)
+#define RUN(AL, NV, MX) launch<add_norm_kernel<T, R, AL, NV, MX>>(dim3(c.blocks), c, 0, s, g)
     SSD_NORM_DISPATCH((sizeof(T) == 4 ? 4 : 2), 1024, RUN);
 #undef RUN
 }
@@ -815,8 +916,8 @@ void run_add_bwd(const AddNormArgs &g, const Cut &c, bool aligned, cudaStream_t 
         add_norm_bwd_wide_kernel<T, R><<<c.blocks, kThreads, 0, s>>>(g);
         return;
     }
-    const size_t sm = g.part ? (size_t)c.threads * c.nv * kVecOf<T> * sizeof(float) : 0;
-#define RUN(AL, NV, MX) add_norm_bwd_kernel<T, R, AL, NV, MX><<<c.blocks, c.threads, sm, s>>>(g)
+    const size_t pb = g.part ? part_bytes(c, kVecOf<T>) : 0;
+#define RUN(AL, NV, MX) launch<add_norm_bwd_kernel<T, R, AL, NV, MX>>(dim3(c.blocks), c, pb, s, g)
     SSD_NORM_DISPATCH((sizeof(T) == 4 ? 4 : 2), 512, RUN);
 #undef RUN
 }
@@ -828,11 +929,12 @@ void run_gated(const GatedNormArgs &g, const Cut &c, bool aligned, cudaStream_t 
         return;
     }
     const dim3 grid(c.blocks, g.groups / c.gpb);
-#define RUN(AL, NV, MX)                                                                    \
-    {                                                                                      \
-        if (!g.z.ptr) gated_norm_kernel<T, AL, kNoGate, NV, MX><<<grid, c.threads, 0, s>>>(g);        \
-        else if (g.after) gated_norm_kernel<T, AL, kGateAfter, NV, MX><<<grid, c.threads, 0, s>>>(g); \
-        else gated_norm_kernel<T, AL, kGateBefore, NV, MX><<<grid, c.threads, 0, s>>>(g);             \
+#define RUN(AL, NV, MX)                                                                         \
+    {                                                                                           \
+        const size_t rb = kRings<AL, MX> ? Ring<2 * NV>::bytes(c.threads) : 0;                  \
+        if (!g.z.ptr) launch<gated_norm_kernel<T, AL, kNoGate, NV, MX>>(grid, c, rb, s, g);      \
+        else if (g.after) launch<gated_norm_kernel<T, AL, kGateAfter, NV, MX>>(grid, c, rb, s, g); \
+        else launch<gated_norm_kernel<T, AL, kGateBefore, NV, MX>>(grid, c, rb, s, g);           \
     }
     SSD_NORM_DISPATCH((sizeof(T) == 4 ? 4 : 2), 1024, RUN);
 #undef RUN
@@ -845,12 +947,13 @@ void run_gated_bwd(const GatedNormArgs &g, const Cut &c, bool aligned, cudaStrea
         return;
     }
     const dim3 grid(c.blocks, g.groups / c.gpb);
-    const size_t sm = g.part ? (size_t)c.threads * c.nv * kVecOf<T> * sizeof(float) : 0;
-#define RUN(AL, NV, MX)                                                                        \
-    {                                                                                          \
-        if (!g.z.ptr) gated_norm_bwd_kernel<T, AL, kNoGate, NV, MX><<<grid, c.threads, sm, s>>>(g);        \
-        else if (g.after) gated_norm_bwd_kernel<T, AL, kGateAfter, NV, MX><<<grid, c.threads, sm, s>>>(g); \
-        else gated_norm_bwd_kernel<T, AL, kGateBefore, NV, MX><<<grid, c.threads, sm, s>>>(g);             \
+    const size_t pb = g.part ? part_bytes(c, kVecOf<T>) : 0;
+#define RUN(AL, NV, MX)                                                                             \
+    {                                                                                               \
+        const size_t rb = kRings<AL, MX> ? Ring<3 * NV>::bytes(c.threads) : 0, sm = rb > pb ? rb : pb; \
+        if (!g.z.ptr) launch<gated_norm_bwd_kernel<T, AL, kNoGate, NV, MX>>(grid, c, sm, s, g);      \
+        else if (g.after) launch<gated_norm_bwd_kernel<T, AL, kGateAfter, NV, MX>>(grid, c, sm, s, g); \
+        else launch<gated_norm_bwd_kernel<T, AL, kGateBefore, NV, MX>>(grid, c, sm, s, g);           \
     }
     SSD_NORM_DISPATCH((sizeof(T) == 4 ? 4 : 2), 512, RUN);
 #undef RUN

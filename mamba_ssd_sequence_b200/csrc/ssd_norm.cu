@@ -15,6 +15,7 @@
 
 #include "ptx.cuh"
 #include "ssd_internal.h"
+#include "ssd_math.cuh"
 #include "ssd_view.h"
 
 namespace ssd {
@@ -101,6 +102,13 @@ struct Raw<T, kVec, false> {
         for (int e = 0; e < kVec; ++e) v[e] = to_f32(q[e]);
     }
 };
+template <typename T, int kVec, bool kAligned>
+__device__ __forceinline__ void get_pairs(const Raw<T, kVec, kAligned> &r, float2 (&v)[kVec / 2]) {
+    float f[kVec];
+    r.get(f);
+#pragma unroll
+    for (int e = 0; e < kVec / 2; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
+}
 template <bool kAligned, typename T, int kVec>
 __device__ __forceinline__ void store(T *p, int left, const float (&v)[kVec]) {
     if constexpr (kAligned) {
@@ -390,13 +398,16 @@ __device__ __forceinline__ float sigmoid(float z) {
     return ptx::rcp_approx(1.0f + e);
 }
 
-// A token's place, walked by a fixed step without a division.
-struct Token {
-    int b, n;
-    __device__ __forceinline__ void advance(int step_b, int step_n, int N) {
-        b += step_b, n += step_n;
-        if (n >= N) n -= N, ++b;
-    }
+// A thread's place in one view, walked by a fixed number of tokens at a time: no
+// division, and one addition a view.
+template <typename T>
+struct Walk {
+    T *p;
+    long long hop, wrap;  // of a step, and when it passes the end of a batch
+    __device__ __forceinline__ Walk(const ssd_view &v, int b, int n, int h, int j, int step_b, int step_n, int N)
+        : p(static_cast<T *>(v.ptr) + b * v.stride_b + n * v.stride_n + h * v.stride_h + j),
+          hop(step_b * v.stride_b + step_n * v.stride_n), wrap(v.stride_b - N * v.stride_n) {}
+    __device__ __forceinline__ void advance(bool wraps) { p += wraps ? hop + wrap : hop; }
 };
 
 enum GateKind { kNoGate = 0, kGateBefore = 1, kGateAfter = 2 };
@@ -470,10 +481,16 @@ struct Ring {
 template <bool kAligned, int kMax>
 constexpr bool kRings = kAligned && kMax <= kThreads;
 
+// SiLU's sigmoid of a pair.
+template <typename T>
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    return make_float2(sigmoid<T>(z.x), sigmoid<T>(z.y));
+}
+
 template <typename T, bool kAligned, int kGate, int kNv, int kMax>
 __global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 ? 3 : 2) : 1)
 gated_norm_kernel(const GatedNormArgs g) {
-    constexpr int kVec = kVecOf<T>;
+    constexpr int kVec = kVecOf<T>, kPairs = kVec / 2;
     constexpr bool kRing = kRings<kAligned, kMax>, has_z = kGate != kNoGate, after = kGate == kGateAfter;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][32];
@@ -486,36 +503,47 @@ gated_norm_kernel(const GatedNormArgs g) {
         const int cl = (lane + i * tpr) * kVec;
         h[i] = (c0 + cl) / g.d, j[i] = (c0 + cl) % g.d, left[i] = g.L - cl;
     }
+    // vector i of a view is this far behind vector 0
+    auto off = [&](const ssd_view &v, int i) { return i ? (h[i] - h[0]) * v.stride_h + (j[i] - j[0]) : 0ll; };
     Ring<2 * kNv> ring(smem);
     const int step_b = (int)(step / g.N), step_n = (int)(step % g.N);
     long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
-    Token here = {(int)(m / g.N), (int)(m % g.N)}, next = here;
-    auto fetch = [&](long long at) {  // of token `next`, which advances
+    const int b = (int)(m / g.N);
+    int n = (int)(m - (long long)b * g.N), n_next = n;
+    Walk<const T> x(g.x, b, n, h[0], j[0], step_b, step_n, g.N), z(g.z, b, n, h[0], j[0], step_b, step_n, g.N);
+    Walk<T> out(g.out, b, n, h[0], j[0], step_b, step_n, g.N);
+    auto passes = [&](int &at) {
+        at += step_n;
+        const bool w = at >= g.N;
+        if (w) at -= g.N;
+        return w;
+    };
+    long long ahead = m;
+    auto fetch = [&]() {  // the next row to come
         if constexpr (kRing) {
-            if (at < tokens) {
-                const T *x = static_cast<const T *>(g.x.ptr) + next.b * g.x.stride_b + next.n * g.x.stride_n;
-                const T *z = static_cast<const T *>(g.z.ptr) + next.b * g.z.stride_b + next.n * g.z.stride_n;
+            if (ahead < tokens) {
 #pragma unroll
                 for (int i = 0; i < kNv; ++i)
                     if (left[i] > 0) {
-                        ring.template copy<T, kVec>(i, x + h[i] * g.x.stride_h + j[i]);
-                        if (has_z) ring.template copy<T, kVec>(kNv + i, z + h[i] * g.z.stride_h + j[i]);
+                        ring.template copy<T, kVec>(i, x.p + off(g.x, i));
+                        if (has_z) ring.template copy<T, kVec>(kNv + i, z.p + off(g.z, i));
                     }
             }
             ring.put_done();
-            next.advance(step_b, step_n, g.N);
+            ahead += step;
+            const bool w = passes(n_next);
+            x.advance(w);
+            if (has_z) z.advance(w);
         }
     };
 #pragma unroll
-    for (int k = 0; k + 1 < ring.kDepth; ++k) fetch(m + k * step);
+    for (int k = 0; k + 1 < ring.kDepth; ++k) fetch();
     int turn = 0;
-    for (; m0 < tokens; m0 += step, m += step, here.advance(step_b, step_n, g.N), ++turn) {
+    for (; m0 < tokens; m0 += step, m += step, ++turn) {
         const bool on = m < tokens;
-        fetch(m + (ring.kDepth - 1) * step);
+        fetch();
         if (kRing) ring.get_wait();
-        const T *x = static_cast<const T *>(g.x.ptr) + here.b * g.x.stride_b + here.n * g.x.stride_n;
-        const T *z = static_cast<const T *>(g.z.ptr) + here.b * g.z.stride_b + here.n * g.z.stride_n;
-        float v[kNv][kVec], ss = 0.0f;
+        float2 v[kNv][kPairs], ss = both(0.0f);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             if (on && left[i] > 0) {
@@ -524,42 +552,50 @@ gated_norm_kernel(const GatedNormArgs g) {
                     ring.load(i, xr);
                     if (has_z) ring.load(kNv + i, zr);
                 } else {
-                    load_heads(xr, x + h[i] * g.x.stride_h + j[i], g.x.stride_h - g.d, j[i], g.d, left[i]);
-                    if (has_z) load_heads(zr, z + h[i] * g.z.stride_h + j[i], g.z.stride_h - g.d, j[i], g.d, left[i]);
+                    load_heads(xr, x.p + off(g.x, i), g.x.stride_h - g.d, j[i], g.d, left[i]);
+                    if (has_z) load_heads(zr, z.p + off(g.z, i), g.z.stride_h - g.d, j[i], g.d, left[i]);
                 }
-                float zv[kVec];
-                xr.get(v[i]);
-                if (has_z) zr.get(zv);
+                float2 zv[kPairs];
+                get_pairs(xr, v[i]);
+                if (has_z) get_pairs(zr, zv);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float s = has_z ? zv[e] * sigmoid<T>(zv[e]) : 1.0f;
-                    const float u = after ? v[i][e] : v[i][e] * s;
-                    ss = fmaf(u, u, ss);
-                    v[i][e] *= s;
+                for (int e = 0; e < kPairs; ++e) {
+                    if (after) ss = fma2(v[i][e], v[i][e], ss);
+                    if (has_z) v[i][e] = mul2(v[i][e], mul2(zv[e], sigmoid2<T>(zv[e])));
+                    if (!after) ss = fma2(v[i][e], v[i][e], ss);
                 }
             }
         }
         ring.get_done();
-        const float rs = rsqrtf(row_sum(ss, tpr, red, turn) / g.L + g.eps);
-        if (!on) continue;
-        T *out = static_cast<T *>(g.out.ptr) + here.b * g.out.stride_b + here.n * g.out.stride_n;
+        const float rs = rsqrtf(row_sum(ss.x + ss.y, tpr, red, turn) / g.L + g.eps);
+        if (on) {
 #pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            if (left[i] > 0) {
-                float w[kVec];
-                load_param<kAligned>(g.w, c0 + g.L - left[i], left[i], 1.0f, w);
+            for (int i = 0; i < kNv; ++i) {
+                if (left[i] > 0) {
+                    float w[kVec];
+                    load_param<kAligned>(g.w, c0 + g.L - left[i], left[i], 1.0f, w);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) v[i][e] = v[i][e] * rs * w[e];
-                store_heads<kAligned>(out + h[i] * g.out.stride_h + j[i], g.out.stride_h - g.d, j[i], g.d, left[i], v[i]);
+                    for (int e = 0; e < kPairs; ++e) {
+                        const float2 y = mul2(mul2(v[i][e], both(rs)), make_float2(w[2 * e], w[2 * e + 1]));
+                        w[2 * e] = y.x, w[2 * e + 1] = y.y;
+                    }
+                    store_heads<kAligned>(out.p + off(g.out, i), g.out.stride_h - g.d, j[i], g.d, left[i], w);
+                }
             }
+            if (g.rstd && lane == 0) g.rstd[m * g.groups + group] = rs;
         }
-        if (g.rstd && lane == 0) g.rstd[m * g.groups + group] = rs;
+        const bool w = passes(n);
+        out.advance(w);
+        if (!kRing) {
+            x.advance(w);
+            if (has_z) z.advance(w);
+        }
     }
 }
 
 template <typename T, bool kAligned, int kGate, int kNv, int kMax>
 __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd_kernel(const GatedNormArgs g) {
-    constexpr int kVec = kVecOf<T>;
+    constexpr int kVec = kVecOf<T>, kPairs = kVec / 2;
     constexpr bool kRing = kRings<kAligned, kMax>, has_z = kGate != kNoGate, after = kGate == kGateAfter;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][32];
@@ -573,98 +609,140 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
         const int cl = (lane + i * tpr) * kVec;
         h[i] = (c0 + cl) / g.d, j[i] = (c0 + cl) % g.d, left[i] = g.L - cl;
     }
+    auto off = [&](const ssd_view &v, int i) { return i ? (h[i] - h[0]) * v.stride_h + (j[i] - j[0]) : 0ll; };
     Ring<3 * kNv> ring(smem);
     const int step_b = (int)(step / g.N), step_n = (int)(step % g.N);
     long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
-    Token here = {(int)(m / g.N), (int)(m % g.N)}, next = here;
-    auto fetch = [&](long long at) {  // of token `next`, which advances
+    const int b = (int)(m / g.N);
+    int n = (int)(m - (long long)b * g.N), n_next = n;
+    Walk<const T> x(g.x, b, n, h[0], j[0], step_b, step_n, g.N), z(g.z, b, n, h[0], j[0], step_b, step_n, g.N),
+        dy(g.dy, b, n, h[0], j[0], step_b, step_n, g.N);
+    Walk<T> dx(g.dx, b, n, h[0], j[0], step_b, step_n, g.N), dz(g.dz, b, n, h[0], j[0], step_b, step_n, g.N);
+    auto passes = [&](int &at) {
+        at += step_n;
+        const bool w = at >= g.N;
+        if (w) at -= g.N;
+        return w;
+    };
+    long long ahead = m;
+    auto fetch = [&]() {  // the next row to come
         if constexpr (kRing) {
-            if (at < tokens) {
-                const T *x = static_cast<const T *>(g.x.ptr) + next.b * g.x.stride_b + next.n * g.x.stride_n;
-                const T *z = static_cast<const T *>(g.z.ptr) + next.b * g.z.stride_b + next.n * g.z.stride_n;
-                const T *dy = static_cast<const T *>(g.dy.ptr) + next.b * g.dy.stride_b + next.n * g.dy.stride_n;
+            if (ahead < tokens) {
 #pragma unroll
                 for (int i = 0; i < kNv; ++i)
                     if (left[i] > 0) {
-                        ring.template copy<T, kVec>(i, x + h[i] * g.x.stride_h + j[i]);
-                        ring.template copy<T, kVec>(kNv + i, dy + h[i] * g.dy.stride_h + j[i]);
-                        if (has_z) ring.template copy<T, kVec>(2 * kNv + i, z + h[i] * g.z.stride_h + j[i]);
+                        ring.template copy<T, kVec>(i, x.p + off(g.x, i));
+                        ring.template copy<T, kVec>(kNv + i, dy.p + off(g.dy, i));
+                        if (has_z) ring.template copy<T, kVec>(2 * kNv + i, z.p + off(g.z, i));
                     }
             }
             ring.put_done();
-            next.advance(step_b, step_n, g.N);
+            ahead += step;
+            const bool w = passes(n_next);
+            x.advance(w), dy.advance(w);
+            if (has_z) z.advance(w);
         }
     };
 #pragma unroll
-    for (int k = 0; k + 1 < ring.kDepth; ++k) fetch(m + k * step);
+    for (int k = 0; k + 1 < ring.kDepth; ++k) fetch();
     float rs_next = m < tokens ? g.rstd[m * g.groups + group] : 0.0f;
     int turn = 0;
-    for (; m0 < tokens; m0 += step, m += step, here.advance(step_b, step_n, g.N), ++turn) {
+    for (; m0 < tokens; m0 += step, m += step, ++turn) {
         const bool on = m < tokens;
         const float rs = rs_next;
         if (m + step < tokens) rs_next = g.rstd[(m + step) * g.groups + group];
-        fetch(m + (ring.kDepth - 1) * step);
+        fetch();
         if (kRing) ring.get_wait();
-        const T *x = static_cast<const T *>(g.x.ptr) + here.b * g.x.stride_b + here.n * g.x.stride_n;
-        const T *z = static_cast<const T *>(g.z.ptr) + here.b * g.z.stride_b + here.n * g.z.stride_n;
-        const T *dy = static_cast<const T *>(g.dy.ptr) + here.b * g.dy.stride_b + here.n * g.dy.stride_n;
-        float xv[kNv][kVec], gy[kNv][kVec], zv[kNv][kVec], sg[kNv][kVec], dot = 0.0f;
+        auto take = [&](int i, float2 (&xv)[kPairs], float2 (&yv)[kPairs]) {
+            Raw<T, kVec, kAligned> xr, yr;
+            if constexpr (kRing) {
+                ring.load(i, xr);
+                ring.load(kNv + i, yr);
+            } else {
+                load_heads(xr, x.p + off(g.x, i), g.x.stride_h - g.d, j[i], g.d, left[i]);
+                load_heads(yr, dy.p + off(g.dy, i), g.dy.stride_h - g.d, j[i], g.d, left[i]);
+            }
+            get_pairs(xr, xv);
+            get_pairs(yr, yv);
+        };
+        // SiLU(z) and its slope are kept over the reduction; x and dy too for one
+        // vector, with more they are read again from where they lie (without the
+        // registers 65536 x 2048 takes 322 us, with spills 458)
+        constexpr bool kHold = kNv == 1;
+        float2 hx[kPairs], hy[kPairs], sl[kNv][kPairs], sp[kNv][kPairs], dot2 = both(0.0f);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             if (on && left[i] > 0) {
-                Raw<T, kVec, kAligned> xr, yr, zr;
-                if constexpr (kRing) {
-                    ring.load(i, xr);
-                    ring.load(kNv + i, yr);
-                    if (has_z) ring.load(2 * kNv + i, zr);
-                } else {
-                    load_heads(xr, x + h[i] * g.x.stride_h + j[i], g.x.stride_h - g.d, j[i], g.d, left[i]);
-                    load_heads(yr, dy + h[i] * g.dy.stride_h + j[i], g.dy.stride_h - g.d, j[i], g.d, left[i]);
-                    if (has_z) load_heads(zr, z + h[i] * g.z.stride_h + j[i], g.z.stride_h - g.d, j[i], g.d, left[i]);
+                float2 xv[kPairs], yv[kPairs], zv[kPairs];
+                take(i, xv, yv);
+                if (kHold) {
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) hx[e] = xv[e], hy[e] = yv[e];
                 }
-                xr.get(xv[i]);
-                yr.get(gy[i]);
-                if (has_z) zr.get(zv[i]);
+                if (has_z) {
+                    Raw<T, kVec, kAligned> zr;
+                    if constexpr (kRing)
+                        ring.load(2 * kNv + i, zr);
+                    else
+                        load_heads(zr, z.p + off(g.z, i), g.z.stride_h - g.d, j[i], g.d, left[i]);
+                    get_pairs(zr, zv);
+                }
                 float w[kVec];
                 load_param<kAligned>(g.w, c0 + g.L - left[i], left[i], 1.0f, w);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    sg[i][e] = has_z ? sigmoid<T>(zv[i][e]) : 1.0f;
-                    const float s = has_z ? zv[i][e] * sg[i][e] : 1.0f;
-                    // xhat (.) g is the same product in both orders of gate and norm
-                    const float t = gy[i][e] * s * (xv[i][e] * rs);
-                    dw[i][e] += t;
-                    gy[i][e] *= w[e];
-                    dot = fmaf(t, w[e], dot);
+                for (int e = 0; e < kPairs; ++e) {
+                    float2 t = mul2(yv[e], mul2(xv[e], both(rs)));  // dy xhat, but for the gate
+                    if (has_z) {
+                        const float2 sig = sigmoid2<T>(zv[e]);
+                        sl[i][e] = mul2(zv[e], sig);
+                        // SiLU' = sig (1 + z (1 - sig)) = sig + SiLU (1 - sig)
+                        sp[i][e] = fma2(sl[i][e], add2(both(1.0f), neg2(sig)), sig);
+                        t = mul2(t, sl[i][e]);
+                    }
+                    dw[i][2 * e] += t.x, dw[i][2 * e + 1] += t.y;
+                    dot2 = fma2(t, make_float2(w[2 * e], w[2 * e + 1]), dot2);
+                }
+            }
+        }
+        const float dot = row_sum(dot2.x + dot2.y, tpr, red, turn) / g.L;
+        if (on) {
+            const float2 rs2 = both(rs), c = both(-rs * dot);
+#pragma unroll
+            for (int i = 0; i < kNv; ++i) {
+                if (left[i] > 0) {
+                    float2 xv[kPairs], yv[kPairs];
+                    if (!kHold) take(i, xv, yv);
+                    float w[kVec], vx[kVec], vz[kVec];
+                    load_param<kAligned>(g.w, c0 + g.L - left[i], left[i], 1.0f, w);
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        const float2 x1 = kHold ? hx[e] : xv[e], gw = mul2(kHold ? hy[e] : yv[e], make_float2(w[2 * e], w[2 * e + 1]));
+                        float2 a, s;
+                        if (!has_z) {
+                            a = mul2(rs2, fma2(x1, c, gw));
+                        } else if (after) {
+                            a = mul2(rs2, fma2(x1, c, mul2(gw, sl[i][e])));
+                            s = mul2(mul2(gw, mul2(x1, rs2)), sp[i][e]);
+                        } else {
+                            const float2 du = mul2(rs2, fma2(mul2(x1, sl[i][e]), c, gw));
+                            a = mul2(du, sl[i][e]);
+                            s = mul2(mul2(du, x1), sp[i][e]);
+                        }
+                        vx[2 * e] = a.x, vx[2 * e + 1] = a.y;
+                        if (has_z) vz[2 * e] = s.x, vz[2 * e + 1] = s.y;
+                    }
+                    store_heads<kAligned>(dx.p + off(g.dx, i), g.dx.stride_h - g.d, j[i], g.d, left[i], vx);
+                    if (has_z) store_heads<kAligned>(dz.p + off(g.dz, i), g.dz.stride_h - g.d, j[i], g.d, left[i], vz);
                 }
             }
         }
         ring.get_done();
-        dot = row_sum(dot, tpr, red, turn) / g.L;
-        if (!on) continue;
-        T *dx = static_cast<T *>(g.dx.ptr) + here.b * g.dx.stride_b + here.n * g.dx.stride_n;
-        T *dz = static_cast<T *>(g.dz.ptr) + here.b * g.dz.stride_b + here.n * g.dz.stride_n;
-#pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            if (left[i] > 0) {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float sig = sg[i][e], s = has_z ? zv[i][e] * sig : 1.0f, xx = xv[i][e], gw = gy[i][e];
-                    float ds;
-                    if (after) {
-                        xv[i][e] = rs * fmaf(-xx * rs, dot, gw * s);
-                        ds = gw * (xx * rs);
-                    } else {
-                        const float du = rs * fmaf(-xx * s * rs, dot, gw);
-                        xv[i][e] = du * s;
-                        ds = du * xx;
-                    }
-                    if (has_z) zv[i][e] = ds * sig * fmaf(zv[i][e], 1.0f - sig, 1.0f);
-                }
-                store_heads<kAligned>(dx + h[i] * g.dx.stride_h + j[i], g.dx.stride_h - g.d, j[i], g.d, left[i], xv[i]);
-                if (has_z)
-                    store_heads<kAligned>(dz + h[i] * g.dz.stride_h + j[i], g.dz.stride_h - g.d, j[i], g.d, left[i], zv[i]);
-            }
+        const bool w = passes(n);
+        dx.advance(w);
+        if (has_z) dz.advance(w);
+        if (!kRing) {
+            x.advance(w), dy.advance(w);
+            if (has_z) z.advance(w);
         }
     }
     if (g.part) {

@@ -116,7 +116,8 @@ __device__ __forceinline__ float2 exact_decay(float2 l, float2 *one_minus) {
 // dt = softplus(p) = max(p, 0) + log1p(u), u = exp(-|p|), with the polynomial
 // of softplus_fast (ssd_math.cuh).
 __device__ __forceinline__ float2 softplus2(float2 p, float2 *u_out) {
-    const float2 u = ex2(make_float2(-fabsf(p.x) * 1.4426950408889634f, -fabsf(p.y) * 1.4426950408889634f));
+    const float2 p2 = mul2(p, both(1.4426950408889634f));
+    const float2 u = ex2(make_float2(-fabsf(p2.x), -fabsf(p2.y)));
     float2 q = both(5.126102362e-03f);
     q = fma2(q, u, both(-2.907406539e-02f));
     q = fma2(q, u, both(7.751608640e-02f));

@@ -2,14 +2,23 @@
 //
 // A cluster takes one block of channels through its sequence in rounds of
 // cluster x tile tokens.  In a round each thread evaluates the gates of its
-// 16-token segment once, keeps a in registers and f x in the place of x and the
-// gate in shared memory, and reduces them to the segment's map h_in -> A h_in + h; the maps are joined over the segments of a
-// warp (shuffles), the warps of a block (shared memory) and the blocks of the
-// cluster (distributed shared memory), which gives each segment its h_in; a
-// second walk then gives h.  So x and the gate are read and
-// h is written once, whatever the number of channels.
+// 16-token segment once, keeps a and f x in registers (x itself is read again
+// where f = 1), and reduces them to the segment's map h_in -> A h_in + h; the
+// maps are joined over the segments of a warp (shuffles), the warps of a block
+// (shared memory) and the blocks of the cluster (distributed shared memory),
+// which gives each segment its h_in; a second walk then gives h.  So x and the
+// gate are read and h is written once, whatever the number of channels, and the
+// result does not depend on timing.
 //
-// Bound by HBM: 6 bytes an element in bf16, 12 in fp32.
+// Floor: HBM, 6 bytes an element in bf16, 12 in fp32.  Measured in bf16: 134M elements
+// in 159 us with a given log-decay, 32 heads of 65536 tokens (clusters of 8;
+// 5.1 TB/s), and in 160 us with softplus gates, 1024 heads of 2048 (5.0 TB/s);
+// 235 us with softplus gates and 32 heads.  What bounds it: the gates'
+// arithmetic (25 to 40 instructions an element; without it 148 and 136 us) and, in
+// clusters, the rounds' exchange (without it 142 us, 204 with softplus gates) with 256
+// blocks on 148 SMs.  Tried and slower: 8 tokens a thread (the work per
+// tile outweighs the higher occupancy: 310 us), blocks of 128 threads, clusters of
+// 16, narrower channel blocks, three stages.
 #include "ssd_glr.cuh"
 
 namespace ssd {
@@ -91,23 +100,23 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         __syncthreads();  // round r has arrived for every thread, and round r - 1 is consumed
         fetch(r + kStages - 1);
         unsigned char *st = sm + (r % kStages) * 2 * Tl::bytes;
-        T *xc = own_column<T, kCb>(st);
+        const T *xc = own_column<T, kCb>(st);
         T *gc = own_column<T, kCb>(st + Tl::bytes);
         const long long t0 = r * round_tok + (long long)rank * Tl::tok + seg * kSeg;
         const int valid = (int)max(0ll, min((long long)kSeg, len - t0));
         if (!M::log && valid < kSeg) close_gates<T, kCb>(gc, valid);
-        float2 a[kSeg], sum = both(0.0f), end = both(0.0f);
+        float2 a[kSeg], u[kPlain ? 1 : kSeg], sum = both(0.0f), end = both(0.0f);
 #pragma unroll
         for (int k = 0; k < kSeg; ++k) {
             const float2 xv = load_pair(xc + k * kCb);
             const Gate o = gate_of<kMode>(load_pair(gc + k * kCb), bias, nrate2);
-            const float2 u = value_of<kMode>(o, xv);
+            const float2 fx = value_of<kMode>(o, xv);
             a[k] = o.a;
             sum = add2(sum, o.l);
-            end = fma2(o.a, end, u);
-            if (!kPlain) keep_pair(xc + k * kCb, gc + k * kCb, u);
+            end = fma2(o.a, end, fx);
+            if (!kPlain) u[k] = fx;
         }
-        auto value = [&](int k) { return kPlain ? load_pair(xc + k * kCb) : kept_pair(xc + k * kCb, gc + k * kCb); };
+        auto value = [&](int k) { return kPlain ? load_pair(xc + k * kCb) : u[kPlain ? 0 : k]; };
         const float4 own = make_map(segment_decay(sum), end);
         float2 hs = enter_segment<T, kCb, true>(own, carry, maps, r, rank, (int)cluster, lost);
         if (states && t0 < g.N) save(t0 / kSeg, hs);

@@ -419,7 +419,8 @@ typedef enum {
  *   states     device, [B, H, ceil(N / SSD_GLR_CHUNK), d_h] fp32, or NULL:
  *              the state before every SSD_GLR_CHUNK-th token, which
  *              ssd_glr_bwd() reads
- * B, H, N, d_h >= 1, any d_h.  Views of any alignment of their element type
+ * B, H, N, d_h >= 1, any d_h; B*H*d_h and N below 2^31 - 65536.  exp(A_log) has
+ * to be finite.  Views of any alignment of their element type
  * are taken; fp32 arrays are 4-byte aligned.  Gates, states and
  * products are fp32; out is rounded once.  Results do not depend on the
  * stream, on other calls or on the layout of the views.

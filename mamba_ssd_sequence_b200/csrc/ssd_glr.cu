@@ -76,7 +76,7 @@ int check_flags(int flags) {
 
 int check_glr(int B, int H, int N, int d, int dtype, int flags, const void *const *f32, int nf32) {
     if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_DTYPE;
-    if (!sizes_ok(B, H, N, d) || (long long)B * H * d >= (1ll << 31)) return SSD_ERR_SHAPE;
+    if (!sizes_ok(B, H, N, d) || (long long)B * H * d >= (1ll << 31) - 65536) return SSD_ERR_SHAPE;
     if (check_flags(flags) != SSD_OK) return SSD_ERR_FLAGS;
     for (int i = 0; i < nf32; ++i)
         if (misaligned(f32[i], 4)) return SSD_ERR_ALIGN;

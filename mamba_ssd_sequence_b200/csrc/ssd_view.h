@@ -9,10 +9,12 @@ namespace ssd {
 
 inline bool misaligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
-// Sizes for which every offset fits 64 bits and every grid its limits.
+// Sizes for which every offset fits 64 bits, every index of a token or channel
+// 32 (rounded up to a tile too) and every grid its limits.
 inline bool sizes_ok(long long B, long long H, long long N, long long d) {
-    return B >= 1 && H >= 1 && N >= 1 && d >= 1 && B * H < (1ll << 31) && H * d < (1ll << 31) &&
-           N < (1ll << 31) - 65536 && B * H * N < (1ll << 40) / d;
+    constexpr long long most = (1ll << 31) - 65536;
+    return B >= 1 && H >= 1 && N >= 1 && d >= 1 && B * H < most && H * d < most && N < most &&
+           B * H * N < (1ll << 40) / d;
 }
 
 // Checks a view of [B, H, N, d].  An output's elements must be distinct: with

@@ -40,7 +40,7 @@ def glr_fwd(lib, **over):
 COMMON = [
     (dict(x=None), NULL), (dict(gate=None), NULL), (dict(x=view(0)), NULL),
     (dict(B=0), SHAPE), (dict(H=0), SHAPE), (dict(N=0), SHAPE), (dict(d=0), SHAPE), (dict(B=-1), SHAPE),
-    (dict(H=1 << 20, d=1 << 20), SHAPE), (dict(B=1 << 20, H=1 << 20), SHAPE), (dict(N=(1 << 31) - 1), SHAPE),
+    (dict(H=1 << 20, d=1 << 20), SHAPE), (dict(B=1 << 20, H=1 << 20), SHAPE), (dict(N=(1 << 31) - 1), SHAPE), (dict(B=1, H=1, N=1, d=(1 << 31) - 8), SHAPE),
     (dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE),
     (dict(flags=8), FLAGS), (dict(flags=-1), FLAGS), (dict(flags=3), FLAGS), (dict(flags=5), FLAGS), (dict(flags=7), FLAGS),
     (dict(x=view(4098)), ALIGN), (dict(x=view(4097), dtype=ssd.SSD_BF16), ALIGN), (dict(A=66), ALIGN),

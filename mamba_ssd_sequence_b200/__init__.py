@@ -12,12 +12,13 @@ built, every call raises -- there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libssd.so")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 
 SSD_F32 = 0
 SSD_BF16 = 1
@@ -396,150 +397,27 @@ def ssd_conv1d(x, w, bias=None, silu: bool = True, out=None, stream=None):
 # enqueued on `stream` (default: the current torch stream); what it allocates
 # belongs to that stream, and tensors given to a call on another stream than
 # the current one are recorded there, so that their memory is not reused early.
+# The calls are compiled (csrc/binding.cpp): the kernel of a decode step is
+# shorter than its checks in Python.
 
-_VIEW = struct.Struct("Pqqq")          # include/ssd.h ssd_view
-_ROWS = struct.Struct("Pq")            # include/ssd.h ssd_rows
-_NORM_PARAMS = struct.Struct("fii")    # include/ssd.h ssd_norm_params
-
-
-torch = None  # imported by the first call
-_F32 = _I32 = _U8 = None
-_CODES = {}
+_binding = None
 
 
-def _import_torch():
-    global torch, _F32, _I32, _U8
-    import torch
-    _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
-    _CODES.update({torch.float32: SSD_F32, torch.bfloat16: SSD_BF16})
-
-
-def _code(t, name) -> int:
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}") from None
-
-
-class _Call:
-    """The device and stream of one call: checks, outputs, the handle."""
-    __slots__ = ("index", "handle", "stream", "used")
-
-    def __init__(self, first, stream):
-        if torch is None:
-            _import_torch()
-        index = first.get_device()
-        if index < 0:
-            raise ValueError("tensors must be on a CUDA device")
-        if torch._C._cuda_getDevice() != index:
-            raise ValueError(f"tensors are on {first.device}, which is not the current CUDA device")
-        self.index, self.stream = index, None
-        self.handle = current = torch._C._cuda_getCurrentRawStream(index)
-        if stream is not None:
-            if stream.device != first.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
-            self.handle = stream.cuda_stream
-            if self.handle != current:
-                self.stream, self.used = stream, []
-
-    def use(self, t, name, shape, dtype):
-        """Checks a tensor and returns its data pointer."""
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.get_device() != self.index:
-            raise ValueError(f"{name} must be on CUDA device {self.index}, got {t.device}")
-        if self.stream is not None:
-            self.used.append(t)
-        return t.data_ptr()
-
-    def flat(self, t, name, shape, dtype):
-        """A contiguous array's pointer, None for None."""
-        if t is None:
-            return None
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return self.use(t, name, shape, dtype)
-
-    def new(self, like, shape, dtype):
-        """An output or workspace tensor that belongs to the call's stream."""
-        if self.stream is None:
-            return like.new_empty(shape, dtype=dtype)
-        with torch.cuda.stream(self.stream):
-            return like.new_empty(shape, dtype=dtype)
-
-    def like(self, t):
-        """A contiguous new tensor of t's shape and type (the quickest one to make)."""
-        if self.stream is None and t.is_contiguous():
-            return torch.empty_like(t)
-        if self.stream is None:
-            return torch.empty_like(t, memory_format=torch.contiguous_format)
-        with torch.cuda.stream(self.stream):
-            return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-    def done(self, rc, where):
-        if self.stream is not None:
-            for t in self.used:
-                t.record_stream(self.stream)
-        if rc != 0:
-            raise SSDError(rc, where)
-
-
-def _spaced(name):
-    return ValueError(f"{name}: the last dimension must be contiguous")
-
-
-def _heads_view(call, t, name, shape, dtype):
-    """ssd_view of a [B, H, N, d_h] tensor."""
-    p = call.use(t, name, shape, dtype)
-    sb, sh, sn, one = t.stride()
-    if one != 1 and shape[3] != 1:
-        raise _spaced(name)
-    return _VIEW.pack(p, sb, sh, sn)
-
-
-def _tokens_view(call, t, name, shape, dtype, d):
-    """ssd_view of a [B, N, H*d_h] tensor, None for None."""
-    if t is None:
-        return None
-    p = call.use(t, name, shape, dtype)
-    sb, sn, one = t.stride()
-    if one != 1 and shape[2] != 1:
-        raise _spaced(name)
-    return _VIEW.pack(p, sb, d, sn)
-
-
-def _rows_view(call, t, name, shape, dtype):
-    """ssd_rows of a [..., C] tensor whose leading dimensions have one stride,
-    None for None."""
-    if t is None:
-        return None
-    p = call.use(t, name, shape, dtype)
-    if t.is_contiguous():
-        return _ROWS.pack(p, shape[-1])
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] != 1:
-        raise _spaced(name)
-    step, n = None, 1
-    for size, stride in zip(reversed(shape[:-1]), reversed(st[:-1])):
-        if size == 1:
-            continue
-        if step is None:
-            step = stride
-        elif stride != step * n:
-            raise ValueError(f"{name}: the leading dimensions must be evenly spaced (one stride between rows)")
-        n *= size
-    return _ROWS.pack(p, shape[-1] if step is None else step)
-
-
-def _glr_gate(dt_p, log_decay, value_dt, value_complement):
-    if (dt_p is None) == (log_decay is None):
-        raise ValueError("give either dt_p or log_decay")
-    if value_dt and (value_complement or dt_p is None):
-        raise ValueError("value_dt needs dt_p, and excludes value_complement")
-    flags = (SSD_VALUE_DT if value_dt else 0) | (SSD_GLR_COMPLEMENT if value_complement else 0)
-    return (dt_p, flags) if log_decay is None else (log_decay, flags | SSD_GLR_LOG_DECAY)
+def load_binding():
+    """Load _binding.so.  Raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        load_library()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is missing: build it with `python -m mamba_ssd_sequence_b200.build`")
+        import torch  # noqa: F401  (its libraries come first)
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(SSDError)
+        _binding = module
+    return _binding
 
 
 def glr_states_shape(B: int, H: int, N: int, d_h: int):
@@ -563,35 +441,13 @@ def ssd_glr_fwd(x, dt_p, A_log, dt_bias, log_decay=None, value_dt: bool = False,
     dt (value_dt) or 1 - a (value_complement).  h0, h_out: [B, H, d_h] float32
     or None; states: alloc_glr_states() to be filled for ssd_glr_bwd; lengths:
     [B] int32, the tokens of each sequence that count."""
-    gate, flags = _glr_gate(dt_p, log_decay, value_dt, value_complement)
-    B, H, N, d = shape = x.shape
-    call = _Call(x, stream)
-    code, dtype = _code(x, "x"), x.dtype
-    if out is None:
-        out = call.like(x)
-    C, state = (H * d,), (B, H, d)
-    rc = load_library().ssd_glr_fwd(
-        _heads_view(call, x, "x", shape, dtype), _heads_view(call, gate, "the gate", shape, dtype),
-        call.flat(A_log, "A_log", C, _F32), call.flat(dt_bias, "dt_bias", C, _F32), call.flat(h0, "h0", state, _F32),
-        call.flat(lengths, "lengths", (B,), _I32), B, H, N, d, code, flags, _heads_view(call, out, "out", shape, dtype),
-        call.flat(h_out, "h_out", state, _F32),
-        None if states is None else call.flat(states, "states", glr_states_shape(B, H, N, d), _F32), call.handle)
-    call.done(rc, "ssd_glr_fwd")
-    return out
+    return (_binding or load_binding()).glr_fwd(x, dt_p, A_log, dt_bias, log_decay, value_dt, value_complement, h0, h_out,
+                                                states, lengths, out, stream)
 
 
 def ssd_glr_bwd_workspace_bytes(B: int, H: int, N: int, d_h: int, dtype: int, flags: int = 0) -> int:
     """Device workspace (bytes) ssd_glr_bwd needs; 0 when invalid."""
     return int(load_library().ssd_glr_bwd_workspace_bytes(B, H, N, d_h, dtype, flags))
-
-
-def _workspace(call, workspace, like, nbytes):
-    """(pointer, bytes) of the given workspace, or of a new one that the
-    caller's frame keeps until the kernels are enqueued."""
-    if workspace is None:
-        workspace = call.new(like, (nbytes or 1,), _U8)
-        return workspace, workspace.data_ptr(), nbytes
-    return workspace, call.flat(workspace, "workspace", workspace.shape, _U8), workspace.numel()
 
 
 def ssd_glr_bwd(dy, x, dt_p, A_log, dt_bias, states, log_decay=None, value_dt: bool = False,
@@ -603,33 +459,8 @@ def ssd_glr_bwd(dy, x, dt_p, A_log, dt_bias, states, log_decay=None, value_dt: b
     of h_out, or None.  Returns (dx, dgate, dA_log, ddt_bias, dh0): dgate is
     the gradient of dt_p or log_decay; dA_log and ddt_bias are None where the
     parameter is."""
-    gate, flags = _glr_gate(dt_p, log_decay, value_dt, value_complement)
-    if states is None:
-        raise ValueError("ssd_glr_bwd needs the states that ssd_glr_fwd saved")
-    B, H, N, d = shape = x.shape
-    call = _Call(x, stream)
-    code, dtype = _code(x, "x"), x.dtype
-    log = bool(flags & SSD_GLR_LOG_DECAY)
-    C, state = (H * d,), (B, H, d)
-    pA, pb = call.flat(A_log, "A_log", C, _F32), call.flat(dt_bias, "dt_bias", C, _F32)
-    dA = None if log or A_log is None else call.like(A_log)
-    db = None if log or dt_bias is None else call.like(dt_bias)
-    dh0 = call.new(states, state, _F32) if dh_out is None else call.like(dh_out)
-    if dx is None:
-        dx = call.like(x)
-    if dgate is None:
-        dgate = call.like(gate)
-    lib = load_library()
-    workspace, pw, nw = _workspace(call, workspace, states, lib.ssd_glr_bwd_workspace_bytes(B, H, N, d, code, flags))
-    rc = lib.ssd_glr_bwd(
-        _heads_view(call, dy, "dy", shape, dtype), _heads_view(call, x, "x", shape, dtype),
-        _heads_view(call, gate, "the gate", shape, dtype), pA, pb,
-        call.flat(states, "states", glr_states_shape(B, H, N, d), _F32), call.flat(lengths, "lengths", (B,), _I32),
-        call.flat(dh_out, "dh_out", state, _F32), B, H, N, d, code, flags, _heads_view(call, dx, "dx", shape, dtype),
-        _heads_view(call, dgate, "dgate", shape, dtype), None if dA is None else dA.data_ptr(),
-        None if db is None else db.data_ptr(), dh0.data_ptr(), pw, nw, call.handle)
-    call.done(rc, "ssd_glr_bwd")
-    return dx, dgate, dA, db, dh0
+    return (_binding or load_binding()).glr_bwd(dy, x, dt_p, A_log, dt_bias, states, log_decay, value_dt, value_complement,
+                                                lengths, dh_out, dx, dgate, workspace, stream)
 
 
 def ssd_glr_step(x, dt_p, A_log, dt_bias, h, log_decay=None, value_dt: bool = False, value_complement: bool = False,
@@ -637,28 +468,8 @@ def ssd_glr_step(x, dt_p, A_log, dt_bias, h, log_decay=None, value_dt: bool = Fa
     """One token of ssd_glr_fwd per sequence (include/ssd.h, ssd_glr_step): x
     and the gate [B, H, d_h]; h [B, H, d_h] float32, updated in place.
     Returns `out` [B, H, d_h]."""
-    gate, flags = _glr_gate(dt_p, log_decay, value_dt, value_complement)
-    if h is None:
-        raise ValueError("ssd_glr_step needs the state h")
-    B, H, d = shape = x.shape
-    call = _Call(x, stream)
-    code, dtype = _code(x, "x"), x.dtype
-    if out is None:
-        out = call.like(x)
-    C = (H * d,)
-
-    def view(t, name):
-        p = call.use(t, name, shape, dtype)
-        sb, sh, one = t.stride()
-        if one != 1 and d != 1:
-            raise _spaced(name)
-        return _VIEW.pack(p, sb, sh, 0)
-
-    rc = load_library().ssd_glr_step(
-        view(x, "x"), view(gate, "the gate"), call.flat(A_log, "A_log", C, _F32), call.flat(dt_bias, "dt_bias", C, _F32),
-        B, H, d, code, flags, call.flat(h, "h", shape, _F32), view(out, "out"), call.handle)
-    call.done(rc, "ssd_glr_step")
-    return out
+    return (_binding or load_binding()).glr_step(x, dt_p, A_log, dt_bias, h, log_decay, value_dt, value_complement, out,
+                                                 stream)
 
 
 def ssd_add_norm(x, residual=None, scale=None, w=None, eps: float = 1e-5, r=None, out=None, rstd=None, stream=None):
@@ -670,28 +481,7 @@ def ssd_add_norm(x, residual=None, scale=None, w=None, eps: float = 1e-5, r=None
     r has the residual's type (it may be given as r=residual, updated in
     place) and is x itself when there is neither residual nor scale; rstd is
     [...] float32, for ssd_add_norm_bwd."""
-    shape = x.shape
-    C = shape[-1]
-    M = x.numel() // C if C else 0
-    call = _Call(x, stream)
-    code, dtype = _code(x, "x"), x.dtype
-    kept, rcode = (dtype, code) if residual is None else (residual.dtype, _code(residual, "residual"))
-    if out is None:
-        out = call.like(x)
-    if rstd is None:
-        rstd = call.new(x, shape[:-1], _F32)
-    plain = residual is None and scale is None
-    if plain and r is not None:
-        raise ValueError("without residual and scale r is x: none is written")
-    if r is None and not plain:
-        r = call.like(x if residual is None else residual)
-    rc = load_library().ssd_add_norm(
-        _rows_view(call, x, "x", shape, dtype), _rows_view(call, residual, "residual", shape, kept),
-        call.flat(scale, "scale", (C,), _F32), call.flat(w, "w", (C,), _F32), M, C, code, rcode,
-        _NORM_PARAMS.pack(eps, 1, 0), _rows_view(call, r, "r", shape, kept), _rows_view(call, out, "out", shape, dtype),
-        call.flat(rstd, "rstd", shape[:-1], _F32), call.handle)
-    call.done(rc, "ssd_add_norm")
-    return out, x if plain else r, rstd
+    return (_binding or load_binding()).add_norm(x, residual, scale, w, eps, r, out, rstd, stream)
 
 
 def ssd_add_norm_bwd(dy, r, rstd, w=None, x=None, scale=None, dres=None, dr=None, dx=None, workspace=None,
@@ -703,30 +493,7 @@ def ssd_add_norm_bwd(dy, r, rstd, w=None, x=None, scale=None, dres=None, dr=None
     scale is given.  Returns (dr, dx, dw, dscale): dr is the gradient of the
     residual, dx of x (dr itself without a scale, when the types are equal);
     dw and dscale are None where the parameter is."""
-    shape = dy.shape
-    C = shape[-1]
-    M = dy.numel() // C if C else 0
-    if scale is not None and x is None:
-        raise ValueError("the gradient of scale needs x")
-    call = _Call(dy, stream)
-    code, rcode, dtype, kept = _code(dy, "dy"), _code(r, "r"), dy.dtype, r.dtype
-    pw, ps = call.flat(w, "w", (C,), _F32), call.flat(scale, "scale", (C,), _F32)
-    if dr is None:
-        dr = call.like(r)
-    if dx is None and not (scale is None and kept is dtype):
-        dx = call.like(dy)
-    dw = None if w is None else call.like(w)
-    ds = None if scale is None else call.like(scale)
-    lib = load_library()
-    workspace, pk, nk = _workspace(call, workspace, rstd, lib.ssd_add_norm_bwd_workspace_bytes(M, C))
-    rc = lib.ssd_add_norm_bwd(
-        _rows_view(call, dy, "dy", shape, dtype), _rows_view(call, r, "r", shape, kept),
-        call.flat(rstd, "rstd", shape[:-1], _F32), pw, None if scale is None else _rows_view(call, x, "x", shape, dtype),
-        ps, _rows_view(call, dres, "dres", shape, kept), M, C, code, rcode, _rows_view(call, dr, "dr", shape, kept),
-        _rows_view(call, dx, "dx", shape, dtype), None if dw is None else dw.data_ptr(),
-        None if ds is None else ds.data_ptr(), pk, nk, call.handle)
-    call.done(rc, "ssd_add_norm_bwd")
-    return dr, dr if dx is None else dx, dw, ds
+    return (_binding or load_binding()).add_norm_bwd(dy, r, rstd, w, x, scale, dres, dr, dx, workspace, stream)
 
 
 def ssd_gated_norm(x, z=None, w=None, groups: int = 1, eps: float = 1e-5, gate_after: bool = False, out=None,
@@ -739,21 +506,7 @@ def ssd_gated_norm(x, z=None, w=None, groups: int = 1, eps: float = 1e-5, gate_a
     token are normalised in `groups` equal groups, of x SiLU(z), or of x with
     the gate applied afterwards (gate_after).  Returns (out [B, N, H*d_h], rstd
     [B, N, groups] float32, for ssd_gated_norm_bwd)."""
-    B, H, N, d = shape = x.shape
-    call = _Call(x, stream)
-    code, dtype = _code(x, "x"), x.dtype
-    tokens, rows = (B, N, H * d), (B, N, groups)
-    if out is None:
-        out = call.new(x, tokens, dtype)
-    if rstd is None:
-        rstd = call.new(x, rows, _F32)
-    rc = load_library().ssd_gated_norm(
-        _heads_view(call, x, "x", shape, dtype), _tokens_view(call, z, "z", tokens, dtype, d),
-        call.flat(w, "w", (H * d,), _F32), B, H, N, d, code,
-        _NORM_PARAMS.pack(eps, groups, SSD_NORM_GATE_AFTER if gate_after else 0),
-        _tokens_view(call, out, "out", tokens, dtype, d), call.flat(rstd, "rstd", rows, _F32), call.handle)
-    call.done(rc, "ssd_gated_norm")
-    return out, rstd
+    return (_binding or load_binding()).gated_norm(x, z, w, groups, eps, gate_after, out, rstd, stream)
 
 
 def ssd_gated_norm_bwd(dy, x, rstd, z=None, w=None, groups: int = 1, gate_after: bool = False, dx=None, dz=None,
@@ -761,25 +514,4 @@ def ssd_gated_norm_bwd(dy, x, rstd, z=None, w=None, groups: int = 1, gate_after:
     """Gradients of ssd_gated_norm (include/ssd.h, ssd_gated_norm_bwd): dy
     [B, N, H*d_h]; the others as there.  Returns (dx [B, H, N, d_h],
     dz [B, N, H*d_h] or None, dw [H*d_h] float32 or None)."""
-    B, H, N, d = shape = x.shape
-    if z is None and dz is not None:
-        raise ValueError("without z there is no dz")
-    call = _Call(x, stream)
-    code, dtype = _code(x, "x"), x.dtype
-    tokens = (B, N, H * d)
-    pw = call.flat(w, "w", (H * d,), _F32)
-    if dx is None:
-        dx = call.like(x)
-    if z is not None and dz is None:
-        dz = call.like(z)
-    dw = None if w is None else call.like(w)
-    lib = load_library()
-    workspace, pk, nk = _workspace(call, workspace, rstd, lib.ssd_gated_norm_bwd_workspace_bytes(B, H, N, d, groups))
-    rc = lib.ssd_gated_norm_bwd(
-        _tokens_view(call, dy, "dy", tokens, dtype, d), _heads_view(call, x, "x", shape, dtype),
-        _tokens_view(call, z, "z", tokens, dtype, d), pw, call.flat(rstd, "rstd", (B, N, groups), _F32), B, H, N, d,
-        code, _NORM_PARAMS.pack(1.0, groups, SSD_NORM_GATE_AFTER if gate_after else 0),
-        _heads_view(call, dx, "dx", shape, dtype), _tokens_view(call, dz, "dz", tokens, dtype, d),
-        None if dw is None else dw.data_ptr(), pk, nk, call.handle)
-    call.done(rc, "ssd_gated_norm_bwd")
-    return dx, dz, dw
+    return (_binding or load_binding()).gated_norm_bwd(dy, x, rstd, z, w, groups, gate_after, dx, dz, workspace, stream)

@@ -1,5 +1,6 @@
 """Builds libssd.so (the CUDA kernels and the C ABI) in-tree with nvcc for
-sm_100a.  Run ``python -m mamba_ssd_sequence_b200.build`` or call build()."""
+sm_100a, and _binding.so (the compiled Python calls of the recurrence and the
+norms) with g++ against torch.  Run ``python -m mamba_ssd_sequence_b200.build`` or call build()."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -14,6 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssd.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -33,14 +36,16 @@ def sources():
 
 
 def _deps_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return max(os.path.getmtime(f) for f in files)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libssd.so; returns its path."""
+    """Compile every csrc/*.cu for sm_100a and link libssd.so, and the compiled
+    calls linked to it; returns the path of libssd.so."""
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+        build_binding()
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     nvcc = _nvcc()
@@ -65,8 +70,37 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp into _binding.so, linked to libssd.so (which has
+    to be there); returns its path."""
+    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include")]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += [BINDING_SRC, "-o", tmp, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(BINDING)

@@ -149,7 +149,7 @@ def test_gated_norm_bwd_codes(lib, over, code):
     assert lib.ssd_gated_norm_bwd_workspace_bytes(1, 2, 3, 4, 8) > 0
 
 
-def test_binding_refuses_host_tensors_and_mixed_options():
+def test_binding_refuses_host_tensors_and_mixed_options(lib):
     x = torch.zeros(1, 2, 4, 16)
     with pytest.raises(ValueError, match="CUDA"):
         ssd.ssd_glr_fwd(x, x, None, None)

@@ -1,5 +1,7 @@
 // Gated linear recurrence: entry points (ssd.h, ssd_glr_fwd / ssd_glr_bwd /
 // ssd_glr_step), the cut of a call into clusters, and the decode step.
+#include <initializer_list>
+
 #include "ssd_glr.cuh"
 
 namespace ssd {
@@ -63,9 +65,14 @@ int mode_of(int flags) {
     return flags & SSD_VALUE_DT ? kDtDt : flags & SSD_GLR_COMPLEMENT ? kDtComplement : kDtNone;
 }
 
-// 16-byte rows: the vector copies and the pairwise stores are possible.
-bool aligned_view(const ssd_view &v, size_t esize) {
-    return !misaligned(v.ptr, 16) && ((v.stride_b | v.stride_h | v.stride_n) * (long long)esize) % 16 == 0;
+// How the views allow their elements to be moved (Args::aligned): by 16 bytes, by
+// two elements, or one by one.
+int alignment_of(std::initializer_list<const ssd_view *> views, int d, size_t esize) {
+    uintptr_t all = (uintptr_t)d * esize;
+    for (const ssd_view *v : views)
+        all |= reinterpret_cast<uintptr_t>(v->ptr) |
+               (uintptr_t)((v->stride_b | v->stride_h | v->stride_n) * (long long)esize);
+    return all % 16 == 0 ? 2 : all % (2 * esize) == 0 ? 1 : 0;
 }
 
 int check_flags(int flags) {
@@ -115,7 +122,7 @@ int ssd_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, con
     g.h_out = h_out;
     g.states = states;
     g.B = B, g.H = H, g.N = N, g.d = d_h;
-    g.aligned = aligned_view(*x, e) && aligned_view(*gate, e) && aligned_view(*out, e) && (d_h * e) % 16 == 0;
+    g.aligned = alignment_of({x, gate, out}, d_h, e);
     const Cut p = cut_of(B, H, N, d_h, dtype);
     g.nblk = p.nblk;
     return launch_fwd(g, p, dtype, mode_of(flags), static_cast<cudaStream_t>(stream));
@@ -162,8 +169,7 @@ int ssd_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, con
     const bool params = dA_log || ddt_bias;
     if (params) g.part = static_cast<float *>(workspace);
     g.B = B, g.H = H, g.N = N, g.d = d_h;
-    g.aligned = aligned_view(*x, e) && aligned_view(*gate, e) && aligned_view(*dy, e) && aligned_view(*dx, e) &&
-                aligned_view(*dgate, e) && (d_h * e) % 16 == 0;
+    g.aligned = alignment_of({dy, x, gate, dx, dgate}, d_h, e);
     const Cut p = cut_of(B, H, N, d_h, dtype);
     g.nblk = p.nblk;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -28,7 +28,9 @@ struct Args {
     const float *A_log, *dt_bias, *h0, *dh_out;
     const int *lengths;
     float *h_out, *states, *dh0, *part;
-    int B, H, N, d, nblk, aligned;
+    int B, H, N, d, nblk;
+    int aligned;  // all views: 2 by 16 bytes, 1 by two elements, 0 by one
+
 };
 
 // Gate kinds and value factors, as template arguments.
@@ -181,6 +183,9 @@ __device__ __forceinline__ int length_of(const int *lengths, int b, int N) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
 __device__ __forceinline__ void cp_async_wait() {
@@ -195,15 +200,56 @@ __device__ __forceinline__ void st_async_f4(uint32_t cluster_addr, uint32_t clus
                  : "memory");
 }
 
+// fetch_tile() of views that are not 16-byte aligned; a call, so that its registers
+// are not taken from the others.
+template <typename T, int kCb>
+__device__ __noinline__ void fetch_unaligned(unsigned char *dst, const T *base, long long stride_n, long long t0, int len,
+                                             int c0, int d, int aligned) {
+    using Tl = Tile<T, kCb>;
+    if (sizeof(T) == 4 || aligned == 1) {
+        constexpr int vec = 4 / sizeof(T), cpr = kCb / vec, per_thread = Tl::tok * cpr / Tl::nt, step = Tl::nt / cpr;
+        const int col = (threadIdx.x % cpr) * vec, row0 = threadIdx.x / cpr;
+        const bool cv = c0 + col < d;
+        const uint32_t s = ptx::smem_u32(dst) + col * (int)sizeof(T);
+#pragma unroll 8
+        for (int i = 0; i < per_thread; ++i) {
+            const int row = row0 + i * step;
+            const bool v = cv && t0 + row < len;
+            cp_async4(s + row / kSeg * Tl::seg + row % kSeg * Tl::row, v ? base + (t0 + row) * stride_n + c0 + col : base, v);
+        }
+    } else {
+        constexpr int per_thread = Tl::tok * kCb / Tl::nt, step = Tl::nt / kCb, batch = 16;
+        static_assert(per_thread % batch == 0, "");
+        const int col = threadIdx.x % kCb, row0 = threadIdx.x / kCb;
+        const bool cv = c0 + col < d;
+        T *out = reinterpret_cast<T *>(dst) + col;
+#pragma unroll 1
+        for (int i0 = 0; i0 < per_thread; i0 += batch) {
+            T v[batch];
+#pragma unroll
+            for (int i = 0; i < batch; ++i) {
+                const long long t = t0 + row0 + (i0 + i) * step;
+                v[i] = cv && t < len ? base[t * stride_n + c0 + col] : T(0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < batch; ++i) {
+                const int row = row0 + (i0 + i) * step;
+                out[(row / kSeg * Tl::seg + row % kSeg * Tl::row) / (int)sizeof(T)] = v[i];
+            }
+        }
+    }
+}
+
 // Fetches a tile of one activation (base: its token 0, channel 0; tokens from
 // t0, channels from c0) into shared memory.  Places at or behind token `len`
-// or channel `d` receive 0.  Aligned views go through asynchronous 16-byte
-// copies, others element by element.
+// or channel `d` receive 0.  Aligned views go through asynchronous copies of 16
+// bytes, others of 4; where those would not be aligned either (bf16 at odd
+// elements), through registers.
 template <typename T, int kCb>
 __device__ __forceinline__ void fetch_tile(unsigned char *dst, const T *base, long long stride_n, long long t0, int len,
-                                           int c0, int d, bool aligned) {
+                                           int c0, int d, int aligned) {
     using Tl = Tile<T, kCb>;
-    if (aligned) {
+    if (aligned == 2) {
         constexpr int vec = 16 / sizeof(T), cpr = kCb / vec, per_thread = Tl::tok * cpr / Tl::nt, step = Tl::nt / cpr;
         constexpr int pad = Tl::seg - kSeg * Tl::row;
         static_assert(step % kSeg == 0 || pad == 0, "the thread's rows are evenly spaced in shared memory");
@@ -223,13 +269,7 @@ __device__ __forceinline__ void fetch_tile(unsigned char *dst, const T *base, lo
             }
         }
     } else {
-        for (int e = threadIdx.x; e < Tl::tok * kCb; e += Tl::nt) {
-            const int row = e / kCb, col = e % kCb;
-            const long long t = t0 + row;
-            T v = T(0.0f);
-            if (t < len && c0 + col < d) v = base[t * stride_n + c0 + col];
-            *reinterpret_cast<T *>(dst + (row / kSeg) * Tl::seg + (row % kSeg) * Tl::row + col * (int)sizeof(T)) = v;
-        }
+        fetch_unaligned<T, kCb>(dst, base, stride_n, t0, len, c0, d, aligned);
     }
 }
 

@@ -37,69 +37,96 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 template <typename T>
 constexpr int kVecOf = 16 / (int)sizeof(T);
 
-template <int kVec>
-__device__ __forceinline__ void store16(float *p, const float (&v)[kVec]) {
+// The words of a vector as it is stored.
+template <typename T, int kVec>
+__device__ __forceinline__ void pack(const float (&v)[kVec], uint32_t (&w)[kVec * sizeof(T) / 4]) {
 #pragma unroll
-    for (int i = 0; i < kVec; i += 4)
-        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
-__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    for (int i = 0; i < kVec * (int)sizeof(T) / 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            w[i] = __float_as_uint(v[i]);
+        } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int kWords>
+__device__ __forceinline__ void store16(void *p, const uint32_t (&w)[kWords]) {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+        static_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
 // kVec channels of a row as they were loaded: the next row's are fetched before
-// the present one is reduced, and take few registers until then.  Rows, views and
-// parameters that are not 16-byte aligned go channel by channel (`left`
-// channels remain to the row's end, the rest reads 0); a thread holds the same
-// channels either way, so the sums have the same bits.
+// the present one is reduced, and take few registers until then.  Where rows,
+// views and parameters are not all 16-byte aligned, each vector goes by the widest
+// loads that its own address allows, and channel by channel at a row's end
+// (`left` channels remain, the rest reads 0); a thread holds the same channels
+// either way, so the sums have the same bits.
 template <typename T, int kVec, bool kAligned>
 struct Raw {
     static constexpr int n = kVec * (int)sizeof(T) / 16;
-    uint4 q[n];
-    __device__ __forceinline__ void load(const T *p, int) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) q[i] = reinterpret_cast<const uint4 *>(p)[i];
-    }
-    __device__ __forceinline__ void get(float (&v)[kVec]) const {
+    uint32_t w[4 * n];
+    __device__ __forceinline__ void load16(const void *p) {
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+            const uint4 q = static_cast<const uint4 *>(p)[i];
+            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+        }
+    }
+    __device__ __forceinline__ void set(int e, T v) {  // element e, from the first on
+        if constexpr (sizeof(T) == 4) {
+            w[e] = __float_as_uint(v);
+        } else {
+            const uint32_t bits = __bfloat16_as_ushort(v);
+            w[e / 2] = e % 2 ? w[e / 2] | bits << 16 : bits;
+        }
+    }
+    __device__ __forceinline__ void load(const T *p, int left) {
+        if constexpr (kAligned) {
+            load16(p);
+        } else {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            if (left >= kVec && at % 16 == 0) {
+                load16(p);
+            } else if (left >= kVec && at % 8 == 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (sizeof(T) == 4) {
-                    v[4 * i + k] = __uint_as_float(w[k]);
-                } else {
-                    v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-                    v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                for (int i = 0; i < 2 * n; ++i) {
+                    const uint2 q = reinterpret_cast<const uint2 *>(p)[i];
+                    w[2 * i] = q.x, w[2 * i + 1] = q.y;
                 }
+            } else if (left >= kVec && at % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < 4 * n; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) set(e, e < left ? p[e] : T(0.0f));
             }
         }
     }
-};
-template <typename T, int kVec>
-struct Raw<T, kVec, false> {
-    T q[kVec];
-    __device__ __forceinline__ void load(const T *p, int left) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) q[e] = e < left ? p[e] : T(0.0f);
-    }
+    // the same across heads of d channels, `hop` apart
     __device__ __forceinline__ void load_heads(const T *p, long long hop, int j, int d, int left) {
+        if (j + kVec <= d) {
+            load(p, left);
+            return;
+        }
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            q[e] = e < left ? *p : T(0.0f);
+            set(e, e < left ? *p : T(0.0f));
             ++p;
             if (++j == d) j = 0, p += hop;
         }
     }
     __device__ __forceinline__ void get(float (&v)[kVec]) const {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = to_f32(q[e]);
+        for (int k = 0; k < 4 * n; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                v[k] = __uint_as_float(w[k]);
+            } else {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+        }
     }
 };
 template <typename T, int kVec, bool kAligned>
@@ -111,12 +138,23 @@ __device__ __forceinline__ void get_pairs(const Raw<T, kVec, kAligned> &r, float
 }
 template <bool kAligned, typename T, int kVec>
 __device__ __forceinline__ void store(T *p, int left, const float (&v)[kVec]) {
+    constexpr int kWords = kVec * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+    pack<T>(v, w);
     if constexpr (kAligned) {
-        store16(p, v);
+        store16(p, w);
     } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        if (left >= kVec && at % 16 == 0) {
+            store16(p, w);
+        } else if (left >= kVec && at % 4 == 0) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e)
-            if (e < left) p[e] = from_f32<T>(v[e]);
+            for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (e < left) p[e] = from_f32<T>(v[e]);
+        }
     }
 }
 // A thread's channels of a per-channel parameter.
@@ -417,14 +455,14 @@ enum GateKind { kNoGate = 0, kGateBefore = 1, kGateAfter = 2 };
 template <typename T, int kVec, bool kAligned>
 __device__ __forceinline__ void load_heads(Raw<T, kVec, kAligned> &q, const T *p, long long hop, int j, int d, int left) {
     if constexpr (kAligned)
-        q.load(p, left);
+        q.load16(p);
     else
         q.load_heads(p, hop, j, d, left);
 }
 template <bool kAligned, typename T, int kVec>
 __device__ __forceinline__ void store_heads(T *p, long long hop, int j, int d, int left, const float (&v)[kVec]) {
-    if constexpr (kAligned) {
-        store16(p, v);
+    if (kAligned || j + kVec <= d) {
+        store<kAligned>(p, left, v);
     } else {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
@@ -472,7 +510,10 @@ struct Ring {
     __device__ __forceinline__ void load(int first, Raw<T, kVec, true> &r) const {
 #pragma unroll
         for (int i = 0; i < Raw<T, kVec, true>::n; ++i)
-            r.q[i] = *reinterpret_cast<const uint4 *>(own + (get * kPer + first + i) * blockDim.x * 16);
+        {
+            const uint4 q = *reinterpret_cast<const uint4 *>(own + (get * kPer + first + i) * blockDim.x * 16);
+            r.w[4 * i] = q.x, r.w[4 * i + 1] = q.y, r.w[4 * i + 2] = q.z, r.w[4 * i + 3] = q.w;
+        }
     }
     __device__ __forceinline__ void get_done() { get = get + 1 == kDepth ? 0 : get + 1; }
 };

@@ -123,7 +123,8 @@ def test_view_results_equal_contiguous_ones(layout):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("B,H,N,d", [
-    (1, 1, 5000, 8), (1, 1, 4099, 64), (1, 3, 2500, 64), (5, 4, 700, 64), (3, 50, 130, 64), (40, 16, 40, 64), (1, 40, 2050, 16)])
+    (1, 1, 5000, 8), (1, 1, 4099, 64), (1, 3, 2500, 64), (5, 4, 700, 64), (3, 50, 130, 64), (40, 16, 40, 64), (1, 40, 2050, 16),
+    (7, 12, 700, 32), (1, 48, 700, 64), (3, 3, 4001, 64), (2, 20, 900, 64)])
 def test_splits_of_the_sequence(B, H, N, d, dtype):
     """From one channel block to more than the SMs hold at once."""
     run_and_check(make(B, H, N, d, dtype, seed=N), "dt", "complement")

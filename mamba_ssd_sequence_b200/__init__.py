@@ -3,11 +3,12 @@ forward operator of Mamba-2 / Mamba-2S / 2Mamba, the gated linear recurrence,
 and the norms around a block.
 
 This module is a thin ctypes binding over libssd.so (C ABI in
-include/ssd.h).  It only marshals arguments: every step of the operator runs
-in the library's CUDA kernels.  Tensors are torch tensors; device tensors
+include/ssd.h); the calls of the recurrence and the norms are compiled
+(csrc/binding.cpp).  Both only marshal arguments: every step of an operator
+runs in the library's CUDA kernels.  Tensors are torch tensors; device tensors
 live on the current CUDA device and are contiguous, except where a function
-takes strided ones.  If libssd.so has not been
-built, every call raises -- there is no fallback implementation.
+takes strided ones.  If libssd.so has not been built, every call raises --
+there is no fallback implementation.
 """
 from __future__ import annotations
 

@@ -11,8 +11,8 @@
 // shared memory.  The second walk, which has l, is a handful of products.
 //
 // Floor: HBM, 10 bytes an element in bf16, 20 in fp32, and the states (0.25).
-// Measured in bf16 with softplus gates: 134M elements in 313 us (1024 heads of 2048
-// tokens; 4.4 TB/s), 16.8M in 62 us (16 heads of 16384, clusters of 8; 2.8 TB/s).
+// Measured in bf16 with softplus gates: 134M elements in 303 us (1024 heads of 2048
+// tokens; 4.5 TB/s), 16.8M in 62 us (16 heads of 16384, clusters of 8; 2.8 TB/s).
 // What bounds it: the arithmetic (without the gates' 253 and 54 us), and in
 // clusters the rounds' exchange (56 us without it).  Evaluating the softplus again
 // in the second walk took 417 and 78 us.

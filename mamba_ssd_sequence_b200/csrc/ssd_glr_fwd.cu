@@ -12,7 +12,7 @@
 //
 // Floor: HBM, 6 bytes an element in bf16, 12 in fp32.  Measured in bf16: 134M elements
 // in 159 us with a given log-decay, 32 heads of 65536 tokens (clusters of 8;
-// 5.1 TB/s), and in 160 us with softplus gates, 1024 heads of 2048 (5.0 TB/s);
+// 5.1 TB/s), and in 162 us with softplus gates, 1024 heads of 2048 (5.0 TB/s);
 // 235 us with softplus gates and 32 heads.  What bounds it: the gates'
 // arithmetic (25 to 40 instructions an element; without it 148 and 136 us) and, in
 // clusters, the rounds' exchange (without it 142 us, 204 with softplus gates) with 256

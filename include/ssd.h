@@ -423,7 +423,9 @@ typedef enum {
  * to be finite.  Views of any alignment of their element type
  * are taken; fp32 arrays are 4-byte aligned.  Gates, states and
  * products are fp32; out is rounded once.  Results do not depend on the
- * stream, on other calls or on the layout of the views.
+ * stream, on other calls or on the layout of the views.  Blocks of a cluster
+ * wait for one another's part for a second at most; if that ran out (never
+ * expected), the outputs that depend on it are NaN.
  * Errors: SSD_ERR_NULL, SSD_ERR_DTYPE, SSD_ERR_SHAPE, SSD_ERR_FLAGS (unknown
  * bits; SSD_VALUE_DT with either of the others), SSD_ERR_ALIGN, SSD_ERR_CUDA.
  */

@@ -177,7 +177,9 @@ __device__ __forceinline__ void load_param(const float *p, int c, int left, floa
 // Rows of more than a warp meet in `red` ([2][32], by the parity of `turn`, so
 // that one barrier a row is enough); every thread of the block calls this.
 __device__ __forceinline__ float row_sum(float v, int tpr, float (*red)[32], int turn) {
-    for (int o = min(tpr, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < tpr) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (tpr <= 32) return v;
     float *r = red[turn & 1];
     const int warp = threadIdx.x / 32, per_row = tpr / 32, first = warp / per_row * per_row;
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 ? 3 :
     const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr;
     const long long step = (long long)gridDim.x * slots;
     const bool has_res = g.res.ptr;
+    const float inv_row = 1.0f / g.C;
     auto at = [&](int i) { return (lane + i * tpr) * kVec; };
     Raw<T, kVec, kAligned> x[kNv];
     Raw<R, kVec, kAligned> res[kNv];
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 ? 3 :
             }
         }
         if (kAhead) fetch(m + step);
-        const float rs = rsqrtf(row_sum(ss, tpr, red, turn) / g.C + g.eps);
+        const float rs = rsqrtf(row_sum(ss, tpr, red, turn) * inv_row + g.eps);
         if (!on) continue;
         R *r = row_of<R>(g.r, m);
         T *out = row_of<T>(g.out, m);
@@ -313,6 +316,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) add_norm_bwd_k
     const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr;
     const long long step = (long long)gridDim.x * slots;
     const bool has_res = g.dres.ptr, has_x = g.x.ptr;
+    const float inv_row = 1.0f / g.C;
     auto at = [&](int i) { return (lane + i * tpr) * kVec; };
     Raw<R, kVec, kAligned> r[kNv], dres[kNv];
     Raw<T, kVec, kAligned> dy[kNv], x[kNv];
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) add_norm_bwd_k
             }
         }
         if (kAhead) fetch(m + step);
-        dot = row_sum(dot, tpr, red, turn) / g.C;
+        dot = row_sum(dot, tpr, red, turn) * inv_row;
         if (!on) continue;
         R *dr = row_of<R>(g.dr, m);
         T *dx = row_of<T>(g.dx, m);
@@ -494,32 +498,36 @@ template <int kPer>
 struct Ring {
     static constexpr int kDepth = kPer <= 8 ? 3 : 2;
     static constexpr size_t bytes(int threads) { return (size_t)kDepth * kPer * threads * 16; }
-    unsigned char *own;
-    int put, get;
+    const unsigned char *own;
+    uint32_t at, piece, put, get;  // own's shared address; bytes between pieces, and of the rows' places
     __device__ __forceinline__ explicit Ring(void *smem)
-        : own(static_cast<unsigned char *>(smem) + threadIdx.x * 16), put(0), get(0) {}
+        : own(static_cast<unsigned char *>(smem) + threadIdx.x * 16), at(ptx::smem_u32(own)), piece(blockDim.x * 16),
+          put(0), get(0) {}
+    __device__ __forceinline__ void next(uint32_t &row) const {
+        row += kPer * piece;
+        if (row == kDepth * kPer * piece) row = 0;
+    }
     // piece `first` on of the row being put: one vector
     template <typename T, int kVec>
-    __device__ __forceinline__ void copy(int first, const T *p) {
+    __device__ __forceinline__ void copy(int first, const T *p) const {
 #pragma unroll
         for (int i = 0; i < Raw<T, kVec, true>::n; ++i)
-            copy16(ptx::smem_u32(own + (put * kPer + first + i) * blockDim.x * 16), reinterpret_cast<const uint4 *>(p) + i);
+            copy16(at + put + (first + i) * piece, reinterpret_cast<const uint4 *>(p) + i);
     }
     __device__ __forceinline__ void put_done() {
         copies_commit();
-        put = put + 1 == kDepth ? 0 : put + 1;
+        next(put);
     }
-    __device__ __forceinline__ void get_wait() { copies_wait<kDepth - 1>(); }
+    __device__ __forceinline__ void get_wait() const { copies_wait<kDepth - 1>(); }
     template <typename T, int kVec>
     __device__ __forceinline__ void load(int first, Raw<T, kVec, true> &r) const {
 #pragma unroll
-        for (int i = 0; i < Raw<T, kVec, true>::n; ++i)
-        {
-            const uint4 q = *reinterpret_cast<const uint4 *>(own + (get * kPer + first + i) * blockDim.x * 16);
+        for (int i = 0; i < Raw<T, kVec, true>::n; ++i) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(own + get + (first + i) * piece);
             r.w[4 * i] = q.x, r.w[4 * i + 1] = q.y, r.w[4 * i + 2] = q.z, r.w[4 * i + 3] = q.w;
         }
     }
-    __device__ __forceinline__ void get_done() { get = get + 1 == kDepth ? 0 : get + 1; }
+    __device__ __forceinline__ void get_done() { next(get); }
 };
 
 // Rows of at most kThreads threads are fetched ahead through a ring.
@@ -542,6 +550,7 @@ gated_norm_kernel(const GatedNormArgs g) {
     const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr / g.gpb;
     const int group = blockIdx.y * g.gpb + slot % g.gpb, c0 = group * g.L;
     const long long tokens = (long long)g.B * g.N, step = (long long)gridDim.x * slots;
+    const float inv_row = 1.0f / g.L;
     int h[kNv], j[kNv], left[kNv];
 #pragma unroll
     for (int i = 0; i < kNv; ++i) {
@@ -612,7 +621,7 @@ gated_norm_kernel(const GatedNormArgs g) {
             }
         }
         ring.get_done();
-        const float rs = rsqrtf(row_sum(ss.x + ss.y, tpr, red, turn) / g.L + g.eps);
+        const float rs = rsqrtf(row_sum(ss.x + ss.y, tpr, red, turn) * inv_row + g.eps);
         if (on) {
 #pragma unroll
             for (int i = 0; i < kNv; ++i) {
@@ -647,6 +656,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
     const int tpr = g.tpr, lane = threadIdx.x % tpr, slot = threadIdx.x / tpr, slots = blockDim.x / tpr / g.gpb;
     const int group = blockIdx.y * g.gpb + slot % g.gpb, c0 = group * g.L;
     const long long tokens = (long long)g.B * g.N, step = (long long)gridDim.x * slots;
+    const float inv_row = 1.0f / g.L;
     int h[kNv], j[kNv], left[kNv];
     float dw[kNv][kVec] = {};
 #pragma unroll
@@ -749,7 +759,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
                 }
             }
         }
-        const float dot = row_sum(dot2.x + dot2.y, tpr, red, turn) / g.L;
+        const float dot = row_sum(dot2.x + dot2.y, tpr, red, turn) * inv_row;
         if (on) {
             const float2 rs2 = both(rs), c = both(-rs * dot);
 #pragma unroll

@@ -9,9 +9,9 @@
 // in shared memory and over the blocks by a second kernel, in a fixed order.
 //
 // Floor: HBM.  Measured in bf16: residual norm of 65536 x 2048 on an fp32 stream 248 us
-// (6.5 TB/s, HBM-bound), its gradients 431 us (5.6 TB/s); gated norm of the
-// same rows 157 us (5.1 TB/s), its gradients 320 us (4.2 TB/s), which issue
-// slots bound: 30 and 44 instructions a channel.
+// (6.5 TB/s, HBM-bound), its gradients 423 us (5.7 TB/s); gated norm of the
+// same rows 147 us (5.5 TB/s), its gradients 312 us (4.3 TB/s), which issue
+// slots bound: 27 and about 40 instructions a channel.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -484,7 +484,7 @@ __device__ __forceinline__ void store_heads(T *p, long long hop, int j, int d, i
 // A thread's own vectors of the rows to come, in shared memory: a ring of kDepth
 // rows of kPer 16-byte pieces a thread, filled by asynchronous copies that take
 // no registers and that only the thread itself waits for.  (Gated norm of 65536 x
-// 2048: 164 us, 196 with one row ahead in registers.  The residual norm moves
+// 2048, when it was added: 164 us, 196 with one row ahead in registers.  The residual norm moves
 // more per channel, and is faster with registers: 248 us, 323 with a ring.)
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -721,8 +721,8 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
             get_pairs(yr, yv);
         };
         // SiLU(z) and its slope are kept over the reduction; x and dy too for one
-        // vector, with more they are read again from where they lie (without the
-        // registers 65536 x 2048 takes 322 us, with spills 458)
+        // vector, with more they are read again from where they lie (65536 x 2048: 322 us
+        // when that was done, 458 with spills)
         constexpr bool kHold = kNv == 1;
         float2 hx[kPairs], hy[kPairs], sl[kNv][kPairs], sp[kNv][kPairs], dot2 = both(0.0f);
 #pragma unroll
@@ -1030,6 +1030,7 @@ void launch(dim3 grid, const Cut &c, size_t smem, cudaStream_t s, const A &g) {
     }
     kernel<<<grid, c.threads, smem, s>>>(g);
 }
+size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 size_t part_bytes(const Cut &c, int vec) { return (size_t)c.threads * c.nv * vec * sizeof(float); }
 
 template <typename T, typename R>
@@ -1083,7 +1084,7 @@ void run_gated_bwd(const GatedNormArgs &g, const Cut &c, bool aligned, cudaStrea
     const size_t pb = g.part ? part_bytes(c, kVecOf<T>) : 0;
 #define RUN(AL, NV, MX)                                                                             \
     {                                                                                               \
-        const size_t rb = kRings<AL, MX> ? Ring<3 * NV>::bytes(c.threads) : 0, sm = rb > pb ? rb : pb; \
+        const size_t sm = larger(kRings<AL, MX> ? Ring<3 * NV>::bytes(c.threads) : 0, pb);            \
         if (!g.z.ptr) launch<gated_norm_bwd_kernel<T, AL, kNoGate, NV, MX>>(grid, c, sm, s, g);      \
         else if (g.after) launch<gated_norm_bwd_kernel<T, AL, kGateAfter, NV, MX>>(grid, c, sm, s, g); \
         else launch<gated_norm_bwd_kernel<T, AL, kGateBefore, NV, MX>>(grid, c, sm, s, g);           \

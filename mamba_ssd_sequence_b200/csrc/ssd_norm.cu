@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 ? 3 :
 }
 
 template <typename T, typename R, bool kAligned, int kNv, int kMax>
-__global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) add_norm_bwd_kernel(const AddNormArgs g) {
+__global__ void __launch_bounds__(kMax, kMax == kThreads ? (sizeof(T) == 2 && kNv == 1 ? 3 : 2) : 1) add_norm_bwd_kernel(const AddNormArgs g) {
     constexpr int kVec = kVecOf<T>;
     constexpr bool kAhead = kMax == kThreads;  // registers for the next row too
     extern __shared__ float sh[];
@@ -970,10 +970,13 @@ constexpr int kSMs = 148;
 constexpr size_t kMaxSmem = 104 * 1024;  // the largest ring: 96 KB
 constexpr unsigned kMaxParts = 4 * kSMs;  // blocks of a backward pass: bounds its workspace
 
-Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward) {
+Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward, bool gated) {
     Cut c{};
     const int vec = (int)(16 / esize), n = (L + vec - 1) / vec, most = backward ? 512 : 1024;
-    c.nv = n <= 32 ? 1 : esize == 4 ? 4 : 2;
+    // the residual norm's gradients in bf16: one vector and three blocks an SM while a
+    // row is at most 128 (8192 x 1024: 27 us, 30 with two vectors and two blocks)
+    const bool light = backward && !gated && esize == 2 && n <= 128;
+    c.nv = n <= 32 || light ? 1 : esize == 4 ? 4 : 2;
     c.tpr = 1;
     while (c.tpr * c.nv < n) c.tpr *= 2;
     c.gpb = 1;
@@ -991,7 +994,7 @@ Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward) {
     while (c.gpb * 2 * c.tpr <= c.threads && groups % (c.gpb * 2) == 0) c.gpb *= 2;
     const long long slots = c.threads / c.tpr / c.gpb, want = (rows + slots - 1) / slots;
     // as many blocks as run at once
-    const int per_sm = backward || esize == 4 ? 2 : 3;
+    const int per_sm = light ? 3 : backward || esize == 4 ? 2 : 3;
     long long most_blocks = (long long)per_sm * kSMs * kThreads / c.threads;
     if (backward && most_blocks > kMaxParts) most_blocks = kMaxParts;
     const unsigned gy = (unsigned)(groups / c.gpb);
@@ -1159,7 +1162,7 @@ int ssd_add_norm(const ssd_rows *x, const ssd_rows *residual, const float *scale
     g.scale = scale, g.w = w, g.rstd = rstd, g.M = M, g.C = C, g.eps = p->eps;
     const bool aligned = rows16(g.x, e) && rows16(g.out, e) && rows16(g.res, er) && rows16(g.r, er) &&
                          !misaligned(scale, 16) && !misaligned(w, 16) && (C * e) % 16 == 0;
-    const Cut c = cut_rows(C, M, 1, e, false);
+    const Cut c = cut_rows(C, M, 1, e, false, false);
     g.tpr = c.tpr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == SSD_F32)
@@ -1206,7 +1209,7 @@ int ssd_add_norm_bwd(const ssd_rows *dy, const ssd_rows *r, const float *rstd, c
     g.want_scale = dscale != nullptr;
     const bool aligned = rows16(g.dy, e) && rows16(g.r, er) && rows16(g.dr, er) && rows16(g.x, e) && rows16(g.dres, er) &&
                          rows16(g.dx, e) && !misaligned(scale, 16) && !misaligned(w, 16) && (C * e) % 16 == 0;
-    const Cut c = cut_rows(C, M, 1, e, true);
+    const Cut c = cut_rows(C, M, 1, e, true, false);
     g.tpr = c.tpr;
     if (dtype == SSD_F32)
         run_add_bwd<float, float>(g, c, aligned, s);
@@ -1241,7 +1244,7 @@ int ssd_gated_norm(const ssd_view *x, const ssd_view *z, const float *w, int B, 
     // a vector lies in one head and one group
     const bool aligned = view16(g.x, e) && view16(g.z, e) && view16(g.out, e) && !misaligned(w, 16) &&
                          (d_h * e) % 16 == 0 && (g.L * e) % 16 == 0;
-    const Cut c = cut_rows(g.L, (long long)B * N, g.groups, e, false);
+    const Cut c = cut_rows(g.L, (long long)B * N, g.groups, e, false, true);
     g.tpr = c.tpr, g.gpb = c.gpb;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == SSD_F32)
@@ -1286,7 +1289,7 @@ int ssd_gated_norm_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *z,
     g.L = H * d_h / p->groups;
     const bool aligned = view16(g.dy, e) && view16(g.x, e) && view16(g.z, e) && view16(g.dx, e) && view16(g.dz, e) &&
                          !misaligned(w, 16) && (d_h * e) % 16 == 0 && (g.L * e) % 16 == 0;
-    const Cut c = cut_rows(g.L, (long long)B * N, g.groups, e, true);
+    const Cut c = cut_rows(g.L, (long long)B * N, g.groups, e, true, true);
     g.tpr = c.tpr, g.gpb = c.gpb;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == SSD_F32)

@@ -9,7 +9,7 @@
 // in shared memory and over the blocks by a second kernel, in a fixed order.
 //
 // Floor: HBM.  Measured in bf16: residual norm of 65536 x 2048 on an fp32 stream 248 us
-// (6.5 TB/s, HBM-bound), its gradients 423 us (5.7 TB/s); gated norm of the
+// (6.5 TB/s, HBM-bound), its gradients 399 us (6.1 TB/s); gated norm of the
 // same rows 147 us (5.5 TB/s), its gradients 312 us (4.3 TB/s), which issue
 // slots bound: 27 and about 40 instructions a channel.
 #include <cuda_bf16.h>
@@ -974,8 +974,9 @@ Cut cut_rows(int L, long long rows, int groups, size_t esize, bool backward, boo
     Cut c{};
     const int vec = (int)(16 / esize), n = (L + vec - 1) / vec, most = backward ? 512 : 1024;
     // the residual norm's gradients in bf16: one vector and three blocks an SM while a
-    // row is at most 128 (8192 x 1024: 27 us, 30 with two vectors and two blocks)
-    const bool light = backward && !gated && esize == 2 && n <= 128;
+    // row is at most a block (8192 x 1024: 27 us, 30 with two vectors and two blocks;
+    // 65536 x 2048 on an fp32 stream: 399 us, 423)
+    const bool light = backward && !gated && esize == 2 && n <= 256;
     c.nv = n <= 32 || light ? 1 : esize == 4 ? 4 : 2;
     c.tpr = 1;
     while (c.tpr * c.nv < n) c.tpr *= 2;

@@ -563,15 +563,9 @@ gated_norm_kernel(const GatedNormArgs g) {
     const int step_b = (int)(step / g.N), step_n = (int)(step % g.N);
     long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
     const int b = (int)(m / g.N);
-    int n = (int)(m - (long long)b * g.N), n_next = n;
+    unsigned n = (unsigned)(m - (long long)b * g.N), n_next = n;
     Walk<const T> x(g.x, b, n, h[0], j[0], step_b, step_n, g.N), z(g.z, b, n, h[0], j[0], step_b, step_n, g.N);
     Walk<T> out(g.out, b, n, h[0], j[0], step_b, step_n, g.N);
-    auto passes = [&](int &at) {
-        at += step_n;
-        const bool w = at >= g.N;
-        if (w) at -= g.N;
-        return w;
-    };
     long long ahead = m;
     auto fetch = [&]() {  // the next row to come
         if constexpr (kRing) {
@@ -585,7 +579,7 @@ gated_norm_kernel(const GatedNormArgs g) {
             }
             ring.put_done();
             ahead += step;
-            const bool w = passes(n_next);
+            const bool w = next_token(n_next, step_n, g.N);
             x.advance(w);
             if (has_z) z.advance(w);
         }
@@ -638,7 +632,7 @@ gated_norm_kernel(const GatedNormArgs g) {
             }
             if (g.rstd && lane == 0) g.rstd[m * g.groups + group] = rs;
         }
-        const bool w = passes(n);
+        const bool w = next_token(n, step_n, g.N);
         out.advance(w);
         if (!kRing) {
             x.advance(w);
@@ -669,16 +663,10 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
     const int step_b = (int)(step / g.N), step_n = (int)(step % g.N);
     long long m0 = (long long)blockIdx.x * slots, m = m0 + slot / g.gpb;
     const int b = (int)(m / g.N);
-    int n = (int)(m - (long long)b * g.N), n_next = n;
+    unsigned n = (unsigned)(m - (long long)b * g.N), n_next = n;
     Walk<const T> x(g.x, b, n, h[0], j[0], step_b, step_n, g.N), z(g.z, b, n, h[0], j[0], step_b, step_n, g.N),
         dy(g.dy, b, n, h[0], j[0], step_b, step_n, g.N);
     Walk<T> dx(g.dx, b, n, h[0], j[0], step_b, step_n, g.N), dz(g.dz, b, n, h[0], j[0], step_b, step_n, g.N);
-    auto passes = [&](int &at) {
-        at += step_n;
-        const bool w = at >= g.N;
-        if (w) at -= g.N;
-        return w;
-    };
     long long ahead = m;
     auto fetch = [&]() {  // the next row to come
         if constexpr (kRing) {
@@ -693,7 +681,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
             }
             ring.put_done();
             ahead += step;
-            const bool w = passes(n_next);
+            const bool w = next_token(n_next, step_n, g.N);
             x.advance(w), dy.advance(w);
             if (has_z) z.advance(w);
         }
@@ -792,7 +780,7 @@ __global__ void __launch_bounds__(kMax, kMax == kThreads ? 2 : 1) gated_norm_bwd
             }
         }
         ring.get_done();
-        const bool w = passes(n);
+        const bool w = next_token(n, step_n, g.N);
         dx.advance(w);
         if (has_z) dz.advance(w);
         if (!kRing) {

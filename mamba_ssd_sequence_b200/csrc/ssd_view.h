@@ -1,4 +1,5 @@
-// Strided activations of the recurrence and the norms: host-side checks.
+// Strided activations of the recurrence and the norms: host-side checks, and the
+// walk over a batch's tokens.
 #pragma once
 
 #include <stdint.h>
@@ -10,7 +11,8 @@ namespace ssd {
 inline bool misaligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 // Sizes for which every offset fits 64 bits, every index of a token or channel
-// 32 (rounded up to a tile too) and every grid its limits.
+// 32 (rounded up to a tile too; the gated norm's steps are larger, see next_token)
+// and every grid its limits.
 inline bool sizes_ok(long long B, long long H, long long N, long long d) {
     constexpr long long most = (1ll << 31) - 65536;
     return B >= 1 && H >= 1 && N >= 1 && d >= 1 && B * H < most && H * d < most && N < most &&
@@ -51,6 +53,19 @@ inline int check_rows(const ssd_rows *v, int M, int C, size_t esize, bool output
     if (!v || !v->ptr) return SSD_ERR_NULL;
     if (v->stride < 0 || (output && M > 1 && v->stride < C)) return SSD_ERR_SHAPE;
     return misaligned(v->ptr, esize) ? SSD_ERR_ALIGN : SSD_OK;
+}
+
+// Moves token n of a batch of N on by step tokens (n, step < N); true where that
+// passes the batch's end, and n is then a token of the next one.  Unsigned, since
+// n + step may pass 2^31 (a step is up to a tenth of all tokens), never 2^32.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline bool next_token(unsigned &n, unsigned step, unsigned N) {
+    n += step;
+    const bool passes = n >= N;
+    if (passes) n -= N;
+    return passes;
 }
 
 inline size_t elem_size(int dtype) { return dtype == SSD_F32 ? 4 : 2; }

@@ -424,8 +424,10 @@ typedef enum {
  * are taken; fp32 arrays are 4-byte aligned.  Gates, states and
  * products are fp32; out is rounded once.  Results do not depend on the
  * stream, on other calls or on the layout of the views.  Blocks of a cluster
- * wait for one another's part for a second at most; if that ran out (never
- * expected), the outputs that depend on it are NaN.
+ * wait for one another's part for a second at most.  If that ran out (never
+ * expected), the block stops taking part, the others run out in their turn, and
+ * all that each writes from then on for tokens and states that count is NaN;
+ * what does not depend on the missing part keeps its value.
  * Errors: SSD_ERR_NULL, SSD_ERR_DTYPE, SSD_ERR_SHAPE, SSD_ERR_FLAGS (unknown
  * bits; SSD_VALUE_DT with either of the others), SSD_ERR_ALIGN, SSD_ERR_CUDA.
  */
@@ -592,6 +594,27 @@ int ssd_debug_fwd(const void *q, const void *k, const void *v,
                   int order, int normalize, int chunk,
                   void *out, void *workspace, size_t workspace_bytes,
                   void *stream, int skip_publish, long long wait_ns, int path);
+
+/*
+ * The same for the recurrence: ssd_glr_fwd() and ssd_glr_bwd() with three
+ * arguments that only failure tests use.
+ *   late_block  0 to 7: this block of each cluster starts late_ns nanoseconds
+ *               late (clusters of fewer blocks are not delayed); -1: none.
+ *               For flags 0 and d_h <= 16 (else SSD_ERR_UNSUPPORTED)
+ *   late_ns     0 to 1e9
+ *   wait_ns     limit of a wait, up to 1e9 (0: the default of one second)
+ * SSD_ERR_SHAPE for values outside these ranges.
+ */
+int ssd_debug_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias,
+                      const float *h0, const int *lengths, int B, int H, int N, int d_h, int dtype, int flags,
+                      const ssd_view *out, float *h_out, float *states, void *stream, int late_block,
+                      long long late_ns, long long wait_ns);
+int ssd_debug_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, const float *A_log,
+                      const float *dt_bias, const float *states, const int *lengths, const float *dh_out,
+                      int B, int H, int N, int d_h, int dtype, int flags, const ssd_view *dx,
+                      const ssd_view *dgate, float *dA_log, float *ddt_bias, float *dh0, void *workspace,
+                      size_t workspace_bytes, void *stream, int late_block, long long late_ns,
+                      long long wait_ns);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *ssd_status_str(int status);

@@ -99,6 +99,10 @@ def load_library():
     lib.ssd_glr_bwd_workspace_bytes.restype = sz
     lib.ssd_glr_bwd.argtypes = [vp] * 8 + [ci] * 6 + [vp] * 6 + [sz, vp]
     lib.ssd_glr_bwd.restype = ci
+    lib.ssd_debug_glr_fwd.argtypes = lib.ssd_glr_fwd.argtypes + [ci, ctypes.c_longlong, ctypes.c_longlong]
+    lib.ssd_debug_glr_fwd.restype = ci
+    lib.ssd_debug_glr_bwd.argtypes = lib.ssd_glr_bwd.argtypes + [ci, ctypes.c_longlong, ctypes.c_longlong]
+    lib.ssd_debug_glr_bwd.restype = ci
     lib.ssd_glr_step.argtypes = [vp] * 4 + [ci] * 5 + [vp] * 3
     lib.ssd_glr_step.restype = ci
     lib.ssd_add_norm.argtypes = [vp] * 4 + [ci] * 4 + [vp] * 5

@@ -72,6 +72,12 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t pari
 }
 constexpr uint32_t kWaitHintNs = 20000;
 
+// Sleeps for ns nanoseconds of wall time (at most about two million naps of a microsecond).
+__device__ __forceinline__ void sleep_for(uint64_t ns) {
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < (1 << 21) && globaltimer_ns() - t0 < ns; ++i) __nanosleep(1000);
+}
+
 // Waits for the phase with the given parity to complete.  Gives up after
 // `limit_ns` nanoseconds of wall time and returns false (the caller records
 // the timeout and leaves); never spins forever.
@@ -152,9 +158,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 // The same without an abort flag.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
     const int never = 0;
-    return mbar_wait_cluster(bar, parity, &never);
+    return mbar_wait_cluster(bar, parity, &never, limit_ns);
 }
 // Store to the shared memory of CTA `rank` of the cluster (address from mapa_shared).
 __device__ __forceinline__ void st_dsmem_u32(uint32_t cluster_addr, uint32_t v) {

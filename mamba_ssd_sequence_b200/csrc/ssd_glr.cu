@@ -88,6 +88,17 @@ int check_flags(int flags) {
     return SSD_OK;
 }
 
+// What the failure tests ask for (ssd_debug_glr_fwd): 0 is the usual limit.
+int set_waits(Args &g, int late_block, long long late_ns, long long wait_ns) {
+    constexpr long long most = 1000000000;
+    if (late_block < -1 || late_block >= kMaxCluster || late_ns < 0 || late_ns > most || wait_ns < 0 || wait_ns > most)
+        return SSD_ERR_SHAPE;
+    g.late = late_block + 1;
+    g.late_ns = late_ns;
+    if (wait_ns) g.wait_ns = wait_ns;
+    return SSD_OK;
+}
+
 int check_glr(int B, int H, int N, int d, int dtype, int flags, const void *const *f32, int nf32) {
     if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_DTYPE;
     if (!sizes_ok(B, H, N, d) || (long long)B * H * d >= (1ll << 31) - 65536) return SSD_ERR_SHAPE;
@@ -106,9 +117,10 @@ using namespace ssd::glr;
 
 extern "C" {
 
-int ssd_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias,
-                const float *h0, const int *lengths, int B, int H, int N, int d_h, int dtype, int flags,
-                const ssd_view *out, float *h_out, float *states, void *stream) {
+int ssd_debug_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias,
+                      const float *h0, const int *lengths, int B, int H, int N, int d_h, int dtype, int flags,
+                      const ssd_view *out, float *h_out, float *states, void *stream, int late_block,
+                      long long late_ns, long long wait_ns) {
     if (!x || !gate || !out) return SSD_ERR_NULL;
     const void *f32[] = {A_log, dt_bias, h0, lengths, h_out, states};
     int rc = check_glr(B, H, N, d_h, dtype, flags, f32, 6);
@@ -118,6 +130,7 @@ int ssd_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, con
         (rc = check_view(out, B, H, N, d_h, e, true)))
         return rc;
     Args g{};
+    if ((rc = set_waits(g, late_block, late_ns, wait_ns))) return rc;
     g.x = *x;
     g.gate = *gate;
     g.out = *out;
@@ -135,17 +148,25 @@ int ssd_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, con
     return launch_fwd(g, p, dtype, mode_of(flags), static_cast<cudaStream_t>(stream));
 }
 
+int ssd_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias,
+                const float *h0, const int *lengths, int B, int H, int N, int d_h, int dtype, int flags,
+                const ssd_view *out, float *h_out, float *states, void *stream) {
+    return ssd_debug_glr_fwd(x, gate, A_log, dt_bias, h0, lengths, B, H, N, d_h, dtype, flags, out, h_out, states, stream,
+                             -1, 0, 0);
+}
+
 size_t ssd_glr_bwd_workspace_bytes(int B, int H, int N, int d_h, int dtype, int flags) {
     if (check_glr(B, H, N, d_h, dtype, flags, nullptr, 0) != SSD_OK) return 0;
     const Cut p = cut_of(B, H, N, d_h, dtype);
     return align_up((size_t)B * p.cluster * H * d_h * 2 * sizeof(float), 256);
 }
 
-int ssd_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, const float *A_log,
-                const float *dt_bias, const float *states, const int *lengths, const float *dh_out,
-                int B, int H, int N, int d_h, int dtype, int flags, const ssd_view *dx,
-                const ssd_view *dgate, float *dA_log, float *ddt_bias, float *dh0, void *workspace,
-                size_t workspace_bytes, void *stream) {
+int ssd_debug_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, const float *A_log,
+                      const float *dt_bias, const float *states, const int *lengths, const float *dh_out,
+                      int B, int H, int N, int d_h, int dtype, int flags, const ssd_view *dx,
+                      const ssd_view *dgate, float *dA_log, float *ddt_bias, float *dh0, void *workspace,
+                      size_t workspace_bytes, void *stream, int late_block, long long late_ns,
+                      long long wait_ns) {
     if (!dy || !x || !gate || !states || !dx || !dgate) return SSD_ERR_NULL;
     const void *f32[] = {A_log, dt_bias, states, lengths, dh_out, dA_log, ddt_bias, dh0};
     int rc = check_glr(B, H, N, d_h, dtype, flags, f32, 8);
@@ -161,6 +182,7 @@ int ssd_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, con
         return SSD_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return SSD_ERR_ALIGN;
     Args g{};
+    if ((rc = set_waits(g, late_block, late_ns, wait_ns))) return rc;
     g.dy = *dy;
     g.x = *x;
     g.gate = *gate;
@@ -183,6 +205,15 @@ int ssd_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, con
     rc = launch_bwd(g, p, dtype, mode_of(flags), s);
     if (rc != SSD_OK || !params) return rc;
     return sum_parts(g.part, (unsigned)(B * p.cluster), 2 * C, (int)C, dA_log, ddt_bias, s);
+}
+
+int ssd_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gate, const float *A_log,
+                const float *dt_bias, const float *states, const int *lengths, const float *dh_out,
+                int B, int H, int N, int d_h, int dtype, int flags, const ssd_view *dx,
+                const ssd_view *dgate, float *dA_log, float *ddt_bias, float *dh0, void *workspace,
+                size_t workspace_bytes, void *stream) {
+    return ssd_debug_glr_bwd(dy, x, gate, A_log, dt_bias, states, lengths, dh_out, B, H, N, d_h, dtype, flags, dx, dgate,
+                             dA_log, ddt_bias, dh0, workspace, workspace_bytes, stream, -1, 0, 0);
 }
 
 int ssd_glr_step(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias, int B,

@@ -30,7 +30,10 @@ struct Args {
     float *h_out, *states, *dh0, *part;
     int B, H, N, d, nblk;
     int aligned;  // all views: 2 by 16 bytes, 1 by two elements, 0 by one
-
+    // limit of a wait, and for tests of it the block of each cluster (plus one; 0 none) that starts late:
+    // a kernel of its own, since the delay takes registers (padded gradients 34.2 us, 33.0 without)
+    long long wait_ns = 1000000000, late_ns = 0;
+    int late = 0;
 };
 
 // Gate kinds and value factors, as template arguments.
@@ -345,12 +348,17 @@ __device__ __forceinline__ void init_maps(M *m, int cluster) {
 // The state (or, kForward false, the adjoint) that enters this thread's
 // segment, given the segment's own map and the carry that enters the round's
 // first tile (the last one, backwards); the carry is advanced over the whole
-// round.  Every thread of the cluster takes part.  A wait that runs out (never
-// expected: the blocks of a cluster run together) makes the carry NaN and is
-// not repeated.
+// round.  Every thread of the cluster takes part.
+//
+// A wait that runs out (never expected: the blocks of a cluster run together)
+// makes the thread's carry NaN from this round on.  Such a thread neither waits
+// nor sends nor announces bytes again: its round's phase is left as it is, and no
+// peer can complete a phase with bytes of another round, or have a map overwritten
+// that it has not read, since nothing is sent of round r + 2 unless all of r + 1
+// has arrived.  Peers that wait for what is not sent run out in their turn.
 template <typename T, int kCb, bool kForward>
 __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, MapsOf<T, kCb> *maps, int round, int rank,
-                                                int cluster, bool &lost) {
+                                                int cluster, long long wait_ns, bool &lost) {
     using Tl = Tile<T, kCb>;
     const int lane = threadIdx.x % Tl::lanes, warp = threadIdx.x / 32, in_warp = (threadIdx.x % 32) / Tl::lanes;
     // the maps of the segments before this one in its warp, and up to it
@@ -381,7 +389,7 @@ __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, MapsO
     }
     // the threads of the tile's last segment join and send the tile's map
     const int two = round & 1;
-    if (warp == (kForward ? Tl::warps - 1 : 0) && in_warp == (kForward ? Tl::per_warp - 1 : 0)) {
+    if (warp == (kForward ? Tl::warps - 1 : 0) && in_warp == (kForward ? Tl::per_warp - 1 : 0) && !lost) {
         float4 all = maps->warp[kForward ? 0 : Tl::warps - 1][lane];
 #pragma unroll
         for (int i = 1; i < Tl::warps - 1; ++i) all = then(all, maps->warp[kForward ? i : Tl::warps - 1 - i][lane]);
@@ -389,10 +397,11 @@ __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, MapsO
         const uint32_t at = ptx::smem_u32(&maps->tile[two][rank][lane]), bar = ptx::smem_u32(&maps->bar[two]);
         for (int r = 0; r < cluster; ++r) st_async_f4(ptx::mapa_shared(at, r), ptx::mapa_shared(bar, r), all);
     }
-    if (!lost) lost = !ptx::mbar_wait_cluster(&maps->bar[two], (round >> 1) & 1);
+    if (!lost) lost = !ptx::mbar_wait_cluster(&maps->bar[two], (round >> 1) & 1, (uint64_t)wait_ns);
     if (lost) carry = both(__uint_as_float(0x7FC00000u));
     // every thread waits for this phase itself; the next one's bytes are announced here
-    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&maps->bar[two], (uint32_t)cluster * sizeof(maps->tile[0][0]));
+    if (threadIdx.x == 0 && !lost)
+        ptx::mbar_arrive_expect_tx(&maps->bar[two], (uint32_t)cluster * sizeof(maps->tile[0][0]));
     float2 h = carry;
     for (int i = 0; i < cluster; ++i) {
         const int r = kForward ? i : cluster - 1 - i;
@@ -405,6 +414,16 @@ __device__ __forceinline__ float2 enter_segment(float4 own, float2 &carry, MapsO
         for (int w = Tl::warps - 1; w > warp; --w) h = apply(maps->warp[w][lane], h);
     }
     return Tl::per_warp > 1 ? apply(before, h) : h;
+}
+
+// The end of a block: no block leaves while a peer may still write to its shared memory.  All
+// is sent by then, and a thread that has waited for every round has received all;
+// one that gave up stays for a millisecond more, for maps that are on their way.
+__device__ __forceinline__ void leave_cluster(int cluster, bool lost) {
+    if (cluster == 1) return;
+    __syncwarp();  // the barrier is for whole warps, whose threads gave up each for itself
+    ptx::cluster_sync_all();
+    if (lost) ptx::sleep_for(1000000);
 }
 
 // How a call is cut up: blocks of cb channels, and `cluster` blocks that share

@@ -39,7 +39,7 @@ constexpr size_t smem_bytes() {
     return (size_t)kStages * 3 * Tl::bytes + sizeof(MapsOf<T, kCb>);
 }
 
-template <typename T, int kCb, int kMode>
+template <typename T, int kCb, int kMode, bool kLate = false>
 __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g) {
     using Tl = Tile<T, kCb>;
     using M = ModeOf<kMode>;
@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
     float2 sumA = make_float2(0.0f, 0.0f), sumb = make_float2(0.0f, 0.0f);
     const float2 nrate = mul2(nrate2, both(0.6931471806f));
 
-    init_maps(maps, (int)cluster);
     bool lost = false;
+    init_maps(maps, (int)cluster);
+    if (kLate && rank + 1 == g.late) ptx::sleep_for((uint64_t)g.late_ns);
     for (int i = 0; i < rounds; ++i) {
         cp_async_wait<kStages - 2>();
         __syncthreads();  // this round has arrived for every thread, and the one before it is consumed
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
             }
         }
         const float4 own = make_map(segment_decay(sum), first);
-        float2 lc = enter_segment<T, kCb, false>(own, carry, maps, i, rank, (int)cluster, lost);
+        float2 lc = enter_segment<T, kCb, false>(own, carry, maps, i, rank, (int)cluster, g.wait_ns, lost);
         if (M::dt) {  // a is evaluated again: kept from above it would take the registers back
 #pragma unroll
             for (int k = 0; k < kSeg; ++k) asm volatile("" : "+f"(c[k].x), "+f"(c[k].y));
@@ -238,14 +239,19 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
             if (on1) part[1] = v.z, part[C + 1] = v.w;
         }
     }
-    // no block leaves while a peer may still write to its shared memory
-    if (cluster > 1) ptx::cluster_sync_all();
+    leave_cluster((int)cluster, lost);
 }
 
 template <typename T, int kCb>
 int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
     constexpr size_t sm = smem_bytes<T, kCb>();
     constexpr int nt = Threads<T>::n;
+    if (g.late) {  // the failure tests' case
+        if constexpr (kCb == 16) {
+            if (mode == kDtNone) return launch_cluster<glr_bwd_kernel<T, kCb, kDtNone, true>>(g, p, nt, sm, s);
+        }
+        return SSD_ERR_UNSUPPORTED;
+    }
     switch (mode) {
     case kDtNone: return launch_cluster<glr_bwd_kernel<T, kCb, kDtNone>>(g, p, nt, sm, s);
     case kDtDt: return launch_cluster<glr_bwd_kernel<T, kCb, kDtDt>>(g, p, nt, sm, s);

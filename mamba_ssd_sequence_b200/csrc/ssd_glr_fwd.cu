@@ -33,7 +33,7 @@ constexpr size_t smem_bytes() {
     return (size_t)kStages * 2 * Tl::bytes + sizeof(MapsOf<T, kCb>);
 }
 
-template <typename T, int kCb, int kMode>
+template <typename T, int kCb, int kMode, bool kLate = false>
 __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g) {
     using Tl = Tile<T, kCb>;
     using M = ModeOf<kMode>;
@@ -93,8 +93,9 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         if (on1) states[chunk * g.d + 1] = v.y;
     };
 
-    init_maps(maps, (int)cluster);
     bool lost = false;
+    init_maps(maps, (int)cluster);
+    if (kLate && rank + 1 == g.late) ptx::sleep_for((uint64_t)g.late_ns);
     for (int r = 0; r < rounds; ++r) {
         cp_async_wait<kStages - 2>();
         __syncthreads();  // round r has arrived for every thread, and round r - 1 is consumed
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         }
         auto value = [&](int k) { return kPlain ? load_pair(xc + k * kCb) : u[kPlain ? 0 : k]; };
         const float4 own = make_map(segment_decay(sum), end);
-        float2 hs = enter_segment<T, kCb, true>(own, carry, maps, r, rank, (int)cluster, lost);
+        float2 hs = enter_segment<T, kCb, true>(own, carry, maps, r, rank, (int)cluster, g.wait_ns, lost);
         if (states && t0 < g.N) save(t0 / kSeg, hs);
         if (g.aligned && valid == kSeg) {
             if (on0) {
@@ -148,14 +149,19 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         if (on0) g.h_out[bc] = carry.x;
         if (on1) g.h_out[bc + 1] = carry.y;
     }
-    // no block leaves while a peer may still write to its shared memory
-    if (cluster > 1) ptx::cluster_sync_all();
+    leave_cluster((int)cluster, lost);
 }
 
 template <typename T, int kCb>
 int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
     constexpr size_t sm = smem_bytes<T, kCb>();
     constexpr int nt = Threads<T>::n;
+    if (g.late) {  // the failure tests' case
+        if constexpr (kCb == 16) {
+            if (mode == kDtNone) return launch_cluster<glr_fwd_kernel<T, kCb, kDtNone, true>>(g, p, nt, sm, s);
+        }
+        return SSD_ERR_UNSUPPORTED;
+    }
     switch (mode) {
     case kDtNone: return launch_cluster<glr_fwd_kernel<T, kCb, kDtNone>>(g, p, nt, sm, s);
     case kDtDt: return launch_cluster<glr_fwd_kernel<T, kCb, kDtDt>>(g, p, nt, sm, s);

@@ -409,17 +409,20 @@ _binding = None
 
 
 def load_binding():
-    """Load _binding.so.  Raises if it has not been built."""
+    """Load _binding.so.  Raises if it has not been built, or against another torch."""
     global _binding
     if _binding is None:
         load_library()
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(
                 f"{BINDING_PATH} is missing: build it with `python -m mamba_ssd_sequence_b200.build`")
-        import torch  # noqa: F401  (its libraries come first)
+        import torch  # its libraries come first
         spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        if module.torch_version != torch.__version__:
+            raise RuntimeError(f"{BINDING_PATH} was built against torch {module.torch_version}, this is "
+                               f"{torch.__version__}: rebuild it with `python -m mamba_ssd_sequence_b200.build`")
         module.set_error(SSDError)
         _binding = module
     return _binding

@@ -1,6 +1,10 @@
 """Builds libssd.so (the CUDA kernels and the C ABI) in-tree with nvcc for
 sm_100a, and _binding.so (the compiled Python calls of the recurrence and the
-norms) with g++ against torch.  Run ``python -m mamba_ssd_sequence_b200.build`` or call build()."""
+norms) with g++ against torch.  Run ``python -m mamba_ssd_sequence_b200.build`` or call build().
+
+libssd.so needs nvcc only.  Where _binding.so cannot be built (no torch, or no
+headers of it), build() warns and everything but the recurrence and the norms
+can be used from Python; build_binding() raises."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -8,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +22,7 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssd.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(OBJDIR, "_binding.txt")  # what it was built against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -43,9 +49,9 @@ def _deps_mtime() -> float:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every csrc/*.cu for sm_100a and link libssd.so, and the compiled
-    calls linked to it; returns the path of libssd.so."""
+    calls linked to it (a warning where that fails); returns the path of libssd.so."""
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
-        build_binding()
+        _try_binding()
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     nvcc = _nvcc()
@@ -70,25 +76,39 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    build_binding(force)
+    _try_binding(force)
     return LIB
+
+
+def _try_binding(force: bool = False) -> None:
+    try:
+        build_binding(force)
+    except Exception as e:
+        if os.path.exists(BINDING):  # out of date: its calls must not be made
+            os.remove(BINDING)
+        warnings.warn(f"{BINDING} was not built: the recurrence and the norms cannot be called from Python ({e})")
 
 
 def build_binding(force: bool = False) -> str:
     """Compile csrc/binding.cpp into _binding.so, linked to libssd.so (which has
-    to be there); returns its path."""
-    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+    to be there), unless it is newer than its sources and was built against this
+    torch and Python; returns its path."""
     import sysconfig
 
     import torch
+    built_for = f"torch {torch.__version__} {os.path.dirname(torch.__file__)} python {sys.version}"
+    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest and os.path.exists(BINDING_FOR):
+        with open(BINDING_FOR) as f:
+            if f.read() == built_for:
+                return BINDING
     from torch.utils import cpp_extension
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     tmp = BINDING + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DSSD_TORCH_VERSION="{torch.__version__}"', "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include")]
     for path in cpp_extension.include_paths():
         cmd += ["-isystem", path]
@@ -98,9 +118,12 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(BINDING_FOR, "w") as f:
+        f.write(built_for)
     return BINDING
 
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
-    print(BINDING)
+    print(build_binding())

@@ -492,6 +492,11 @@ def ssd_add_norm(x, residual=None, scale=None, w=None, eps: float = 1e-5, r=None
     return (_binding or load_binding()).add_norm(x, residual, scale, w, eps, r, out, rstd, stream)
 
 
+def ssd_add_norm_bwd_workspace_bytes(M: int, C: int) -> int:
+    """Device workspace (bytes) ssd_add_norm_bwd needs for M rows of C channels; 0 when invalid."""
+    return int(load_library().ssd_add_norm_bwd_workspace_bytes(M, C))
+
+
 def ssd_add_norm_bwd(dy, r, rstd, w=None, x=None, scale=None, dres=None, dr=None, dx=None, workspace=None,
                      stream=None):
     """Gradients of ssd_add_norm (include/ssd.h, ssd_add_norm_bwd).
@@ -515,6 +520,11 @@ def ssd_gated_norm(x, z=None, w=None, groups: int = 1, eps: float = 1e-5, gate_a
     the gate applied afterwards (gate_after).  Returns (out [B, N, H*d_h], rstd
     [B, N, groups] float32, for ssd_gated_norm_bwd)."""
     return (_binding or load_binding()).gated_norm(x, z, w, groups, eps, gate_after, out, rstd, stream)
+
+
+def ssd_gated_norm_bwd_workspace_bytes(B: int, H: int, N: int, d_h: int, groups: int = 1) -> int:
+    """Device workspace (bytes) ssd_gated_norm_bwd needs; 0 when invalid."""
+    return int(load_library().ssd_gated_norm_bwd_workspace_bytes(B, H, N, d_h, groups))
 
 
 def ssd_gated_norm_bwd(dy, x, rstd, z=None, w=None, groups: int = 1, gate_after: bool = False, dx=None, dz=None,

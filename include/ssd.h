@@ -422,7 +422,9 @@ typedef enum {
  * B, H, N, d_h >= 1, any d_h; B*H*d_h and N below 2^31 - 65536.  exp(A_log) has
  * to be finite.  Views of any alignment of their element type
  * are taken; fp32 arrays are 4-byte aligned.  Gates, states and
- * products are fp32; out is rounded once.  Results do not depend on the
+ * products are fp32; out is rounded once.  In units of 2^-24 and relative, with
+ * p = gate + dt_bias: dt is off by up to 8 + 0.05 |p| for fp32 activations and by
+ * 8 + |p| for bf16 ones, a by up to 3 + (9 + 2 |p|) |log a|.  Results do not depend on the
  * stream, on other calls or on the layout of the views.  Blocks of a cluster
  * wait for one another's part for a second at most.  If that ran out (never
  * expected), the block stops taking part, the others run out in their turn, and

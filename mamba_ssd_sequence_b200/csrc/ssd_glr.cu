@@ -35,9 +35,9 @@ namespace {
 constexpr int kThreads = 128;
 
 // One token of one channel (both halves of the pairwise forms take it).
-template <int kMode>
+template <typename T, int kMode>
 __device__ __forceinline__ float step(float g, float bias, float nrate2, float x, float h) {
-    const Gate o = gate_of<kMode>(both(g), both(bias), both(nrate2));
+    const Gate o = gate_of<T, kMode>(both(g), both(bias), both(nrate2));
     float2 w;
     const float a = exact_decay(o.l, &w).x;  // steps follow one another: as exact as a segment's product
     return fmaf(a, h, value_of<kMode>(o, both(x)).x);
@@ -55,11 +55,11 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(const Args g, int mo
     const float nrate2 = -1.4426950408889634f * (g.A_log ? expf(g.A_log[c]) : 1.0f), bias = g.dt_bias ? g.dt_bias[c] : 0.0f;
     float y;
     switch (mode) {
-    case kDtNone: y = step<kDtNone>(gv, bias, nrate2, xv, h0); break;
-    case kDtDt: y = step<kDtDt>(gv, bias, nrate2, xv, h0); break;
-    case kDtComplement: y = step<kDtComplement>(gv, bias, nrate2, xv, h0); break;
-    case kLogNone: y = step<kLogNone>(gv, bias, nrate2, xv, h0); break;
-    default: y = step<kLogComplement>(gv, bias, nrate2, xv, h0); break;
+    case kDtNone: y = step<T, kDtNone>(gv, bias, nrate2, xv, h0); break;
+    case kDtDt: y = step<T, kDtDt>(gv, bias, nrate2, xv, h0); break;
+    case kDtComplement: y = step<T, kDtComplement>(gv, bias, nrate2, xv, h0); break;
+    case kLogNone: y = step<T, kLogNone>(gv, bias, nrate2, xv, h0); break;
+    default: y = step<T, kLogComplement>(gv, bias, nrate2, xv, h0); break;
     }
     g.h_out[i] = y;
     store_one(static_cast<T *>(g.out.ptr) + b * g.out.stride_b + h * g.out.stride_h + j, y);

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
 #pragma unroll
         for (int k = 0; k < kSeg; ++k) {
             const float2 xv = load_pair(xc + k * kCb), yv = load_pair(yc + k * kCb);
-            const Gate o = gate_of<kMode>(load_pair(gc + k * kCb), bias, nrate2);
+            const Gate o = gate_of<T, kMode>(load_pair(gc + k * kCb), bias, nrate2);
             const float2 q = mul2(o.a, M::complement ? add2(hs, neg2(xv)) : hs);
             hs = fma2(o.a, hs, value_of<kMode>(o, xv));
             sum = add2(sum, o.l);
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
             } else {
                 if (M::complement) c[k] = make_float2(pack_decay(o.a.x, o.f.x), pack_decay(o.a.y, o.f.y));
                 r[k] = mul2(slope_of(o), M::dt ? fma2(nrate, q, xv) : mul2(nrate, q));
+                // the logarithm is kept finite, so that its product with a = 0 is 0
                 keep_pair(xc + k * kCb, gc + k * kCb,
                           mul2(q, make_float2(fmaxf(o.l.x, -3.0e38f), fmaxf(o.l.y, -3.0e38f))));
             }

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
 #pragma unroll
         for (int k = 0; k < kSeg; ++k) {
             const float2 xv = load_pair(xc + k * kCb);
-            const Gate o = gate_of<kMode>(load_pair(gc + k * kCb), bias, nrate2);
+            const Gate o = gate_of<T, kMode>(load_pair(gc + k * kCb), bias, nrate2);
             const float2 fx = value_of<kMode>(o, xv);
             a[k] = o.a;
             sum = add2(sum, o.l);

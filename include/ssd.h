@@ -601,10 +601,11 @@ int ssd_debug_fwd(const void *q, const void *k, const void *v,
  * The same for the recurrence: ssd_glr_fwd() and ssd_glr_bwd() with three
  * arguments that only failure tests use.
  *   late_block  0 to 7: this block of each cluster starts late_ns nanoseconds
- *               late (clusters of fewer blocks are not delayed); -1: none.
- *               For flags 0 and d_h <= 16 (else SSD_ERR_UNSUPPORTED)
+ *               late (clusters of fewer blocks are not delayed), for flags 0 and
+ *               d_h <= 16 (else SSD_ERR_UNSUPPORTED); -1: none (the call is
+ *               then ssd_glr_fwd() or ssd_glr_bwd())
  *   late_ns     0 to 1e9
- *   wait_ns     limit of a wait, up to 1e9 (0: the default of one second)
+ *   wait_ns     limit of a wait with a late block, up to 1e9 (0: one second)
  * SSD_ERR_SHAPE for values outside these ranges.
  */
 int ssd_debug_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias,

@@ -88,15 +88,13 @@ int check_flags(int flags) {
     return SSD_OK;
 }
 
-// What the failure tests ask for (ssd_debug_glr_fwd): 0 is the usual limit.
-int set_waits(Args &g, int late_block, long long late_ns, long long wait_ns) {
-    constexpr long long most = 1000000000;
-    if (late_block < -1 || late_block >= kMaxCluster || late_ns < 0 || late_ns > most || wait_ns < 0 || wait_ns > most)
-        return SSD_ERR_SHAPE;
-    g.late = late_block + 1;
-    g.late_ns = late_ns;
-    if (wait_ns) g.wait_ns = wait_ns;
-    return SSD_OK;
+// What the failure tests ask for (ssd_debug_glr_fwd).
+bool late_ok(int late_block, long long late_ns, long long wait_ns) {
+    return late_block >= -1 && late_block < kMaxCluster && late_ns >= 0 && late_ns <= kWaitNs && wait_ns >= 0 &&
+           wait_ns <= kWaitNs;
+}
+LateArgs late_args(const Args &g, int late_block, long long late_ns, long long wait_ns) {
+    return {g, wait_ns ? wait_ns : kWaitNs, late_ns, late_block};
 }
 
 int check_glr(int B, int H, int N, int d, int dtype, int flags, const void *const *f32, int nf32) {
@@ -129,8 +127,8 @@ int ssd_debug_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_lo
     if ((rc = check_view(x, B, H, N, d_h, e, false)) || (rc = check_view(gate, B, H, N, d_h, e, false)) ||
         (rc = check_view(out, B, H, N, d_h, e, true)))
         return rc;
+    if (!late_ok(late_block, late_ns, wait_ns)) return SSD_ERR_SHAPE;
     Args g{};
-    if ((rc = set_waits(g, late_block, late_ns, wait_ns))) return rc;
     g.x = *x;
     g.gate = *gate;
     g.out = *out;
@@ -145,7 +143,8 @@ int ssd_debug_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_lo
     g.aligned = alignment_of({x, gate, out}, d_h, e);
     const Cut p = cut_of(B, H, N, d_h, dtype);
     g.nblk = p.nblk;
-    return launch_fwd(g, p, dtype, mode_of(flags), static_cast<cudaStream_t>(stream));
+    const LateArgs late = late_args(g, late_block, late_ns, wait_ns);
+    return launch_fwd(g, late_block < 0 ? nullptr : &late, p, dtype, mode_of(flags), static_cast<cudaStream_t>(stream));
 }
 
 int ssd_glr_fwd(const ssd_view *x, const ssd_view *gate, const float *A_log, const float *dt_bias,
@@ -181,8 +180,8 @@ int ssd_debug_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gat
     if (!workspace || workspace_bytes < ssd_glr_bwd_workspace_bytes(B, H, N, d_h, dtype, flags))
         return SSD_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return SSD_ERR_ALIGN;
+    if (!late_ok(late_block, late_ns, wait_ns)) return SSD_ERR_SHAPE;
     Args g{};
-    if ((rc = set_waits(g, late_block, late_ns, wait_ns))) return rc;
     g.dy = *dy;
     g.x = *x;
     g.gate = *gate;
@@ -202,7 +201,8 @@ int ssd_debug_glr_bwd(const ssd_view *dy, const ssd_view *x, const ssd_view *gat
     const Cut p = cut_of(B, H, N, d_h, dtype);
     g.nblk = p.nblk;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    rc = launch_bwd(g, p, dtype, mode_of(flags), s);
+    const LateArgs late = late_args(g, late_block, late_ns, wait_ns);
+    rc = launch_bwd(g, late_block < 0 ? nullptr : &late, p, dtype, mode_of(flags), s);
     if (rc != SSD_OK || !params) return rc;
     return sum_parts(g.part, (unsigned)(B * p.cluster), 2 * C, (int)C, dA_log, ddt_bias, s);
 }

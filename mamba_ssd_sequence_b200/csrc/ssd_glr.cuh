@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "ssd_internal.h"
@@ -30,11 +31,32 @@ struct Args {
     float *h_out, *states, *dh0, *part;
     int B, H, N, d, nblk;
     int aligned;  // all views: 2 by 16 bytes, 1 by two elements, 0 by one
-    // limit of a wait, and for tests of it the block of each cluster (plus one; 0 none) that starts late:
-    // a kernel of its own, since the delay takes registers (padded gradients 34.2 us, 33.0 without)
-    long long wait_ns = 1000000000, late_ns = 0;
-    int late = 0;
 };
+
+// The failure tests' kernels: one block of each cluster starts late, and a wait has a
+// limit of its own.  Kernels and arguments apart from the others', since the delay takes
+// registers (padded gradients 34.2 us, 33.0 without) and longer arguments a launch's time
+// (a decode step 4.0 us, 3.65 without).
+constexpr long long kWaitNs = 1000000000;  // the usual limit
+struct LateArgs : Args {
+    long long wait_ns, late_ns;
+    int late;
+};
+template <bool kLate>
+using ArgsOf = std::conditional_t<kLate, LateArgs, Args>;
+template <bool kLate>
+__device__ __forceinline__ long long wait_limit(const ArgsOf<kLate> &g) {
+    if constexpr (kLate)
+        return g.wait_ns;
+    else
+        return kWaitNs;
+}
+template <bool kLate>
+__device__ __forceinline__ void start_late(const ArgsOf<kLate> &g, int rank) {
+    if constexpr (kLate) {
+        if (rank == g.late) ptx::sleep_for((uint64_t)g.late_ns);
+    }
+}
 
 // Gate kinds and value factors, as template arguments.
 enum Mode { kDtNone = 0, kDtDt = 1, kDtComplement = 2, kLogNone = 3, kLogComplement = 4 };
@@ -455,13 +477,14 @@ struct Cut {
 };
 Cut cut_of(int B, int H, int N, int d, int dtype);
 
-int launch_fwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s);
-int launch_bwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s);
+// `late`: the failure tests' kernel, or NULL (the others are then those of Args).
+int launch_fwd(const Args &g, const LateArgs *late, const Cut &p, int dtype, int mode, cudaStream_t s);
+int launch_bwd(const Args &g, const LateArgs *late, const Cut &p, int dtype, int mode, cudaStream_t s);
 
 // Launches a kernel in clusters.  Its shared memory limit is set once per CUDA
 // context (the driver never reuses a context's ID).
-template <auto kernel>
-int launch_cluster(const Args &g, const Cut &p, int threads, size_t smem, cudaStream_t s) {
+template <auto kernel, typename A>
+int launch_cluster(const A &g, const Cut &p, int threads, size_t smem, cudaStream_t s) {
     static std::atomic<unsigned long long> set_in{0};
     unsigned long long id = 0;
     if (!current_context_id(&id) || set_in.load(std::memory_order_relaxed) != id + 1) {

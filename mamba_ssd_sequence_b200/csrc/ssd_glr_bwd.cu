@@ -40,7 +40,7 @@ constexpr size_t smem_bytes() {
 }
 
 template <typename T, int kCb, int kMode, bool kLate = false>
-__global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g) {
+__global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const ArgsOf<kLate> g) {
     using Tl = Tile<T, kCb>;
     using M = ModeOf<kMode>;
     extern __shared__ __align__(128) unsigned char sm[];
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
 
     bool lost = false;
     init_maps(maps, (int)cluster);
-    if (kLate && rank + 1 == g.late) ptx::sleep_for((uint64_t)g.late_ns);
+    start_late<kLate>(g, rank);
     for (int i = 0; i < rounds; ++i) {
         cp_async_wait<kStages - 2>();
         __syncthreads();  // this round has arrived for every thread, and the one before it is consumed
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
             }
         }
         const float4 own = make_map(segment_decay(sum), first);
-        float2 lc = enter_segment<T, kCb, false>(own, carry, maps, i, rank, (int)cluster, g.wait_ns, lost);
+        float2 lc = enter_segment<T, kCb, false>(own, carry, maps, i, rank, (int)cluster, wait_limit<kLate>(g), lost);
         if (M::dt) {  // a is evaluated again: kept from above it would take the registers back
 #pragma unroll
             for (int k = 0; k < kSeg; ++k) asm volatile("" : "+f"(c[k].x), "+f"(c[k].y));
@@ -244,12 +244,12 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_bwd_kernel(const Args g)
 }
 
 template <typename T, int kCb>
-int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
+int launch_mode(const Args &g, const LateArgs *late, const Cut &p, int mode, cudaStream_t s) {
     constexpr size_t sm = smem_bytes<T, kCb>();
     constexpr int nt = Threads<T>::n;
-    if (g.late) {  // the failure tests' case
+    if (late) {
         if constexpr (kCb == 16) {
-            if (mode == kDtNone) return launch_cluster<glr_bwd_kernel<T, kCb, kDtNone, true>>(g, p, nt, sm, s);
+            if (mode == kDtNone) return launch_cluster<glr_bwd_kernel<T, kCb, kDtNone, true>>(*late, p, nt, sm, s);
         }
         return SSD_ERR_UNSUPPORTED;
     }
@@ -263,15 +263,15 @@ int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
 }
 
 template <typename T>
-int launch_cb(const Args &g, const Cut &p, int mode, cudaStream_t s) {
-    return p.cb == 64 ? launch_mode<T, 64>(g, p, mode, s)
-                      : p.cb == 32 ? launch_mode<T, 32>(g, p, mode, s) : launch_mode<T, 16>(g, p, mode, s);
+int launch_cb(const Args &g, const LateArgs *late, const Cut &p, int mode, cudaStream_t s) {
+    return p.cb == 64 ? launch_mode<T, 64>(g, late, p, mode, s)
+                      : p.cb == 32 ? launch_mode<T, 32>(g, late, p, mode, s) : launch_mode<T, 16>(g, late, p, mode, s);
 }
 
 }  // namespace
 
-int launch_bwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s) {
-    return dtype == SSD_F32 ? launch_cb<float>(g, p, mode, s) : launch_cb<__nv_bfloat16>(g, p, mode, s);
+int launch_bwd(const Args &g, const LateArgs *late, const Cut &p, int dtype, int mode, cudaStream_t s) {
+    return dtype == SSD_F32 ? launch_cb<float>(g, late, p, mode, s) : launch_cb<__nv_bfloat16>(g, late, p, mode, s);
 }
 
 }  // namespace glr

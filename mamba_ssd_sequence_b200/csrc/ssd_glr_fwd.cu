@@ -34,7 +34,7 @@ constexpr size_t smem_bytes() {
 }
 
 template <typename T, int kCb, int kMode, bool kLate = false>
-__global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g) {
+__global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const ArgsOf<kLate> g) {
     using Tl = Tile<T, kCb>;
     using M = ModeOf<kMode>;
     constexpr bool kPlain = kMode == kDtNone || kMode == kLogNone;  // f x is x
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
 
     bool lost = false;
     init_maps(maps, (int)cluster);
-    if (kLate && rank + 1 == g.late) ptx::sleep_for((uint64_t)g.late_ns);
+    start_late<kLate>(g, rank);
     for (int r = 0; r < rounds; ++r) {
         cp_async_wait<kStages - 2>();
         __syncthreads();  // round r has arrived for every thread, and round r - 1 is consumed
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
         }
         auto value = [&](int k) { return kPlain ? load_pair(xc + k * kCb) : u[kPlain ? 0 : k]; };
         const float4 own = make_map(segment_decay(sum), end);
-        float2 hs = enter_segment<T, kCb, true>(own, carry, maps, r, rank, (int)cluster, g.wait_ns, lost);
+        float2 hs = enter_segment<T, kCb, true>(own, carry, maps, r, rank, (int)cluster, wait_limit<kLate>(g), lost);
         if (states && t0 < g.N) save(t0 / kSeg, hs);
         if (g.aligned && valid == kSeg) {
             if (on0) {
@@ -153,12 +153,12 @@ __global__ void __launch_bounds__(Threads<T>::n, 2) glr_fwd_kernel(const Args g)
 }
 
 template <typename T, int kCb>
-int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
+int launch_mode(const Args &g, const LateArgs *late, const Cut &p, int mode, cudaStream_t s) {
     constexpr size_t sm = smem_bytes<T, kCb>();
     constexpr int nt = Threads<T>::n;
-    if (g.late) {  // the failure tests' case
+    if (late) {
         if constexpr (kCb == 16) {
-            if (mode == kDtNone) return launch_cluster<glr_fwd_kernel<T, kCb, kDtNone, true>>(g, p, nt, sm, s);
+            if (mode == kDtNone) return launch_cluster<glr_fwd_kernel<T, kCb, kDtNone, true>>(*late, p, nt, sm, s);
         }
         return SSD_ERR_UNSUPPORTED;
     }
@@ -172,15 +172,15 @@ int launch_mode(const Args &g, const Cut &p, int mode, cudaStream_t s) {
 }
 
 template <typename T>
-int launch_cb(const Args &g, const Cut &p, int mode, cudaStream_t s) {
-    return p.cb == 64 ? launch_mode<T, 64>(g, p, mode, s)
-                      : p.cb == 32 ? launch_mode<T, 32>(g, p, mode, s) : launch_mode<T, 16>(g, p, mode, s);
+int launch_cb(const Args &g, const LateArgs *late, const Cut &p, int mode, cudaStream_t s) {
+    return p.cb == 64 ? launch_mode<T, 64>(g, late, p, mode, s)
+                      : p.cb == 32 ? launch_mode<T, 32>(g, late, p, mode, s) : launch_mode<T, 16>(g, late, p, mode, s);
 }
 
 }  // namespace
 
-int launch_fwd(const Args &g, const Cut &p, int dtype, int mode, cudaStream_t s) {
-    return dtype == SSD_F32 ? launch_cb<float>(g, p, mode, s) : launch_cb<__nv_bfloat16>(g, p, mode, s);
+int launch_fwd(const Args &g, const LateArgs *late, const Cut &p, int dtype, int mode, cudaStream_t s) {
+    return dtype == SSD_F32 ? launch_cb<float>(g, late, p, mode, s) : launch_cb<__nv_bfloat16>(g, late, p, mode, s);
 }
 
 }  // namespace glr

@@ -506,6 +506,8 @@ typedef struct {
  *   p          eps (groups and flags are not used)
  * res_dtype is `dtype` or SSD_F32.  The norm is of r as stored, so a later
  * reader of the stream sees what was normalised.  Sums are fp32.
+ * A row whose sum of squares leaves fp32 (values near 2^64) normalises to 0.  But
+ * for r, outputs must not overlap an input.
  * M, C >= 1.  Errors: SSD_ERR_NULL, SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes,
  * strides, eps), SSD_ERR_ALIGN (element alignment), SSD_ERR_CUDA.
  */
@@ -530,6 +532,7 @@ size_t ssd_add_norm_bwd_workspace_bytes(int M, int C);
  *          with equal types it equals dr)
  *   dw, dscale  device, [C] fp32, or NULL
  *   workspace   device, >= ssd_add_norm_bwd_workspace_bytes(), 256-byte aligned
+ * But for dr, outputs must not overlap an input.
  */
 int ssd_add_norm_bwd(const ssd_rows *dy, const ssd_rows *r, const float *rstd, const float *w,
                      const ssd_rows *x, const float *scale, const ssd_rows *dres, int M, int C, int dtype,
@@ -548,8 +551,8 @@ int ssd_add_norm_bwd(const ssd_rows *dy, const ssd_rows *r, const float *rstd, c
  *   out    device view, `dtype`: stride_h = d_h, stride_n = H*d_h writes the
  *          rows that an output projection reads
  *   rstd   device, [B, N, groups] fp32, or NULL
- * groups divides H*d_h (SSD_ERR_SHAPE otherwise).  Errors as ssd_add_norm(),
- * plus SSD_ERR_FLAGS.
+ * groups divides H*d_h and is at most 65535 (SSD_ERR_SHAPE otherwise).  Outputs
+ * must not overlap an input.  Errors as ssd_add_norm(), plus SSD_ERR_FLAGS.
  */
 int ssd_gated_norm(const ssd_view *x, const ssd_view *z, const float *w, int B, int H, int N, int d_h,
                    int dtype, const ssd_norm_params *p, const ssd_view *out, float *rstd, void *stream);

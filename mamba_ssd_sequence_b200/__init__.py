@@ -403,7 +403,9 @@ def ssd_conv1d(x, w, bias=None, silu: bool = True, out=None, stream=None):
 # belongs to that stream, and tensors given to a call on another stream than
 # the current one are recorded there, so that their memory is not reused early.
 # The calls are compiled (csrc/binding.cpp): the kernel of a decode step is
-# shorter than its checks in Python.
+# shorter than its checks in Python.  Like ssd_fwd they record nothing for
+# automatic differentiation: outputs do not require grad, and gradients come from
+# the _bwd calls.
 
 _binding = None
 

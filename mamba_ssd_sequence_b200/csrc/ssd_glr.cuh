@@ -136,7 +136,7 @@ __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ptx::ex2_ap
 // a = 2^l.  The hardware exponential is off by 1.4e-7 at most, but by -2e-8 on
 // the mean (measured over l in [-0.5, 0]), which adds up over the many tokens
 // that a slow decay spans.  So a segment's product of decays is evaluated
-// from the sum of its l, near 1 by the polynomial (decay_of), and the
+// from the sum of its l, near 1 by the polynomial (segment_decay), and the
 // hardware's error acts within a segment only.
 __device__ __forceinline__ float2 exact_decay(float2 l, float2 *one_minus) {
     const float2 la = mul2(l, both(0.6931471806f)), q = decay_poly(la), e = ex2(l);

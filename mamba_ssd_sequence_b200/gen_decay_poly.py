@@ -1,5 +1,5 @@
 """Generates the coefficients of the polynomial q with 1 - exp(-t) ~ t q(t)
-on [-1/2, 1/2] that the gated linear recurrence (csrc/ssd_glr.cuh, decay_of)
+on [-1/2, 1/2] that the gated linear recurrence (csrc/ssd_glr.cuh, exact_decay)
 uses: Chebyshev interpolation of (1 - exp(-t)) / t at the degree + 1 Chebyshev
 nodes, converted to powers of t and rounded to float32.  Prints the
 coefficients (constant term first) and the largest relative error of t q(t)
